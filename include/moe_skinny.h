@@ -86,7 +86,11 @@ typedef enum {
   MOE_EHIP = 4
 } moe_status_t;
 
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype_t;
+typedef enum {
+  MOE_DT_F32 = 0,
+  MOE_DT_BF16 = 1,
+  MOE_DT_E4M3 = 2   /* OCP 8-bit float, 3 mantissa bits, no infinity; only where a call names it */
+} moe_dtype_t;
 
 typedef enum {
   MOE_VARIANT_AUTO = 0,
@@ -103,7 +107,9 @@ typedef enum {
   MOE_OP_ROUTE = 1,
   MOE_OP_EXPERT_FFN = 2,
   MOE_OP_BLOCK = 3,
-  MOE_OP_ROUTE_LATENT = 4
+  MOE_OP_ROUTE_LATENT = 4,
+  MOE_OP_SKINNY_GEMM_FP8 = 5,
+  MOE_OP_BLOCK_FP8 = 6
 } moe_op_t;
 
 /* Version of this ABI (MOE_ABI_VERSION). */
@@ -170,7 +176,9 @@ int moe_plan_words(int B, int k, int E);
  *   MOE_OP_ROUTE:       dtype, B, d, E, k
  *   MOE_OP_EXPERT_FFN:  dtype, B, d, E, k, I, Is
  *   MOE_OP_BLOCK:       dtype, B, d, E, k, I, Is
- *   MOE_OP_ROUTE_LATENT: dtype, B, d, E, k, and N = L (the latent rows) */
+ *   MOE_OP_ROUTE_LATENT: dtype, B, d, E, k, and N = L (the latent rows)
+ *   MOE_OP_SKINNY_GEMM_FP8: dtype (of X), B, N, K
+ *   MOE_OP_BLOCK_FP8:   dtype, B, d, E, k, I, Is */
 size_t moe_workspace_bytes(int op, int dtype, int B, int d, int E, int k, int I, int Is, int N,
                            int K);
 
@@ -418,6 +426,74 @@ moe_status_t moe_block_noalloc(int dtype, int B, int d, int E, int k, int I, int
                                const void* Wr, const float* bias, int bias_ld, const void* W13,
                                const void* W2, const void* Ws13, const void* Ws2, void* out,
                                int32_t* topk_ids, float* topk_w, void* stream);
+
+/* ---- 8-bit weights ---------------------------------------------------------
+ * The dense product and the whole block over weights in OCP e4m3 with one
+ * fp32 scale for each 128 x 128 block (blocks at the lower and right edges
+ * are shorter): a value is its code times its block's scale.  Half the bytes
+ * of bf16, which is what bounds a small decode batch. */
+
+/* Scale groups of moe_quantize_fp8. */
+typedef enum {
+  MOE_FP8_ROWS = 0,    /* each 128 columns of one row (activations) */
+  MOE_FP8_BLOCKS = 1   /* each 128 x 128 block (weights) */
+} moe_fp8_layout_t;
+
+/* n matrices X [n][rows][cols] (dtype: bf16 or fp32) to e4m3 codes Q
+ * [n][rows][cols] and fp32 scales: [n][rows][ceil(cols / 128)] (MOE_FP8_ROWS)
+ * or [n][ceil(rows / 128)][ceil(cols / 128)] (MOE_FP8_BLOCKS).
+ *   scale = the smallest power of two, at least 2^-126, with
+ *   max|x| / scale <= 448 over the group (1 where the group holds zeros
+ *   only); q = x / scale rounded to nearest, ties to even.  Infinities and
+ *   NaN do not enter the maximum and become NaN.
+ *   cols a multiple of 16; less than 2^31 scales (rows) or 2^24 (blocks).  Q
+ *   and scale must not overlap X. */
+moe_status_t moe_quantize_fp8(int layout, int dtype, int n, int rows, int cols, const void* X, void* Q, float* scale,
+                              void* stream);
+
+/* skinny_gemm over 8-bit weights, with skinny_gemm_residual's R when non-null:
+ *   Y[b][n] = sum_c X[b][c] * W[n][c] * w_scale[n / 128][c / 128] (+ R[b][n]),
+ *   each 128-column block summed in fp32, then added to the fp32 sum of the
+ *   row by its scale.
+ *   X [B][K]: bf16 (x_scale NULL), or e4m3 with x_scale [B][ceil(K / 128)],
+ *   which then multiplies too.  W [N][K] e4m3, w_scale
+ *   [ceil(N / 128)][ceil(K / 128)], R [B][N] bf16, Y [B][N] bf16 or fp32.
+ *   Y may be R itself (bf16) but must not otherwise overlap an input.
+ *   1 <= B <= 64, K a multiple of 16 up to 65536, N up to 2^24.  Workspace:
+ *   moe_workspace_bytes(MOE_OP_SKINNY_GEMM_FP8, x_dtype, B, ..., N, K) bytes
+ *   as for skinny_gemm; ws may be NULL when 0.  One kernel shape: the forced
+ *   variants do not apply. */
+moe_status_t skinny_gemm_fp8(int x_dtype, int B, int N, int K, const void* X, const float* x_scale, const void* W,
+                             const float* w_scale, const void* R, void* Y, int y_dtype, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* The experts of moe_block_fp8 (device pointers in a host struct, read before
+ * the call returns).  Gate and up rows have blocks of their own: one row of
+ * scales for each 128 gate rows, then for each 128 up rows.  Ws13 NULL: no
+ * shared expert (the other shared pointers are then ignored). */
+typedef struct {
+  const void* W13;     /* e4m3 [E][2I][d] */
+  const float* s13;    /* [E][2 ceil(I / 128)][ceil(d / 128)] */
+  const void* W2;      /* e4m3 [E][d][I] */
+  const float* s2;     /* [E][ceil(d / 128)][ceil(I / 128)] */
+  const void* Ws13;    /* e4m3 [2Is][d] */
+  const float* ss13;   /* [2 ceil(Is / 128)][ceil(d / 128)] */
+  const void* Ws2;     /* e4m3 [d][Is] */
+  const float* ss2;    /* [ceil(d / 128)][ceil(Is / 128)] */
+} moe_fp8_experts_t;
+
+/* moe_block with the routed and shared experts in 8 bits.  X, Wr and out are
+ * bf16 (dtype MOE_DT_BF16); routing, weights, the shared expert and the
+ * combine are moe_block's, ids and weights bit for bit those of moe_block on
+ * the same X, Wr and bias.  Scope and errors: those of moe_block, and d up to
+ * 65536.  Two launches at B <= 2, three while B * k <= 64 and B <= 8, else
+ * the router's one or two and two.  MOE_SCHEDULE_LAUNCHES keeps the router
+ * in a launch of its own, MOE_SCHEDULE_FUSED is MOE_EUNSUPPORTED; forced
+ * variants apply to the router.  Workspace:
+ * moe_workspace_bytes(MOE_OP_BLOCK_FP8, ...). */
+moe_status_t moe_block_fp8(int dtype, int B, int d, int E, int k, int I, int Is, const void* X, const void* Wr,
+                           const float* bias, int bias_ld, const moe_fp8_experts_t* experts, void* out,
+                           int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

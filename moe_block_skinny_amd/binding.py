@@ -17,9 +17,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_skinny.so")
 
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = range(5)
-DT_F32, DT_BF16 = 0, 1
+DT_F32, DT_BF16, DT_E4M3 = 0, 1, 2
 VARIANT_AUTO, VARIANT_GEMV, VARIANT_SPLITK, VARIANT_MFMA, VARIANT_ROWS = range(5)
-OP_SKINNY_GEMM, OP_ROUTE, OP_EXPERT_FFN, OP_BLOCK, OP_ROUTE_LATENT = range(5)
+(OP_SKINNY_GEMM, OP_ROUTE, OP_EXPERT_FFN, OP_BLOCK, OP_ROUTE_LATENT, OP_SKINNY_GEMM_FP8,
+ OP_BLOCK_FP8) = range(7)
 KERNEL_ROUTE, KERNEL_EXPERT_UP, KERNEL_EXPERT_DOWN, KERNEL_COMBINE, KERNEL_SKINNY, KERNEL_BLOCK, KERNEL_STREAM = range(7)
 VARIANTS = {"auto": VARIANT_AUTO, "gemv": VARIANT_GEMV, "splitk": VARIANT_SPLITK, "mfma": VARIANT_MFMA, "rows": VARIANT_ROWS}
 SCHEDULE_AUTO, SCHEDULE_LAUNCHES, SCHEDULE_FUSED, SCHEDULE_ROUTER_IN_UP = range(4)
@@ -27,6 +28,9 @@ SCHEDULES = {"auto": SCHEDULE_AUTO, "launches": SCHEDULE_LAUNCHES, "fused": SCHE
              "router_in_up": SCHEDULE_ROUTER_IN_UP}
 SHARED_AUTO, SHARED_IN_UP, SHARED_IN_ROUTER = range(3)
 SHARED_SCHEDULES = {"auto": SHARED_AUTO, "up": SHARED_IN_UP, "router": SHARED_IN_ROUTER}
+FP8_ROWS, FP8_BLOCKS = range(2)
+FP8_LAYOUTS = {"rows": FP8_ROWS, "blocks": FP8_BLOCKS}
+FP8_BLOCK = 128   # columns (and weight rows) that share a scale
 
 # name: (restype, argtypes)
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -54,6 +58,9 @@ SIGNATURES = {
     "moe_block": (_I, [_I] * 7 + [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_block_streams": (_I, [_I] * 7 + [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P, _P, _P, _P]),
     "moe_block_noalloc": (_I, [_I] * 7 + [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_quantize_fp8": (_I, [_I] * 5 + [_P] * 4),
+    "skinny_gemm_fp8": (_I, [_I] * 4 + [_P] * 6 + [_I, _P, _Z, _P]),
+    "moe_block_fp8": (_I, [_I] * 7 + [_P, _P, _P, _I, _P, _P, _P, _P, _P, _Z, _P]),
 }
 
 
@@ -444,3 +451,176 @@ def prefetch(tensors, sink, stream=None):
     ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
     sizes = (ctypes.c_size_t * n)(*[t.numel() * t.element_size() for t in tensors])
     _check(lib.moe_prefetch(n, ptrs, sizes, _ptr(sink), sink.numel(), _stream(stream)))
+
+
+# ---- 8-bit weights ---------------------------------------------------------------
+
+
+def _groups(n):
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _on(name, t, shape, dtype, device):
+    """The checks of _Args.arr and on_gpu for one tensor of a call whose device is known."""
+    if not isinstance(t, torch.Tensor):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        raise TypeError("%s: a torch.Tensor expected, got %s" % (name, type(t).__name__))
+    if t.shape != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if t.dtype != dtype:
+        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.device != device:
+        if t.device.type != "cuda":
+            raise ValueError("%s must be in GPU memory (device %s)" % (name, t.device))
+        raise ValueError("%s is on %s, the other arguments on %s" % (name, t.device, device))
+    return t.data_ptr()
+
+
+def _device_of(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: a torch.Tensor expected, got %s" % (name, type(t).__name__))
+    return t.device
+
+
+def _call(device, f, stream, *args):
+    """f(*args, stream) with `device` current: a launch goes to the current device, and without a stream to the
+    stream that is current there."""
+    if device.type != "cuda":
+        raise ValueError("the arguments must be in GPU memory (device %s)" % device)
+    if torch.cuda.current_device() == device.index:
+        _check(f(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, _stream(stream)))
+
+
+class Fp8Weight:
+    """A weight matrix in 8 bits: codes [N][K] (float8_e4m3fn) and fp32 scales [ceil(N/128)][ceil(K/128)], as
+    moe_quantize_fp8 leaves them in its "blocks" layout.  Checked here once; holds both tensors."""
+
+    def __init__(self, codes, scale):
+        self.N, self.K = _shape("codes", codes, 2)
+        self.device = codes.device
+        a = _Args()
+        a.arr("codes", codes, (self.N, self.K), torch.float8_e4m3fn)
+        a.arr("scale", scale, (_groups(self.N), _groups(self.K)), torch.float32)
+        a.on_gpu()
+        self.codes, self.scale = codes.detach(), scale.detach()
+        self._ptrs = (self.codes.data_ptr(), self.scale.data_ptr())
+
+
+class _ExpertsStruct(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("W13", "s13", "W2", "s2", "Ws13", "ss13", "Ws2", "ss2")]
+
+
+class Fp8Experts:
+    """The experts of moe_block_fp8: codes (float8_e4m3fn) W13 [E][2I][d], W2 [E][d][I] and, with a shared
+    expert, Ws13 [2Is][d], Ws2 [d][Is], each with its fp32 scales: one row for each 128 gate rows, then for each
+    128 up rows (s13 [E][2 ceil(I/128)][ceil(d/128)], ss13 alike), s2 [E][ceil(d/128)][ceil(I/128)], ss2 alike.
+    Checked here once; holds the tensors."""
+
+    def __init__(self, W13, s13, W2, s2, Ws13=None, ss13=None, Ws2=None, ss2=None):
+        self.E, two_i, self.d = _shape("W13", W13, 3)
+        if two_i % 2:
+            raise ValueError("W13: [E][2I][d] expected, got %s" % (tuple(W13.shape),))
+        E, d, I = self.E, self.d, two_i // 2
+        self.I, self.Is, self.device = I, 0, W13.device
+        f8, f32 = torch.float8_e4m3fn, torch.float32
+        a = _Args()
+        a.arr("W13", W13, (E, 2 * I, d), f8)
+        a.arr("s13", s13, (E, 2 * _groups(I), _groups(d)), f32)
+        a.arr("W2", W2, (E, d, I), f8)
+        a.arr("s2", s2, (E, _groups(d), _groups(I)), f32)
+        given = [t is not None for t in (Ws13, ss13, Ws2, ss2)]
+        if any(given):
+            if not all(given):
+                raise ValueError("Ws13, ss13, Ws2 and ss2 come together (all or none)")
+            two_s, _ = _shape("Ws13", Ws13, 2)
+            if two_s % 2:
+                raise ValueError("Ws13: [2Is][d] expected, got %s" % (tuple(Ws13.shape),))
+            Is = self.Is = two_s // 2
+            a.arr("Ws13", Ws13, (2 * Is, d), f8)
+            a.arr("ss13", ss13, (2 * _groups(Is), _groups(d)), f32)
+            a.arr("Ws2", Ws2, (d, Is), f8)
+            a.arr("ss2", ss2, (_groups(d), _groups(Is)), f32)
+        a.on_gpu()
+        self.tensors = [None if t is None else t.detach() for t in (W13, s13, W2, s2, Ws13, ss13, Ws2, ss2)]
+        self._struct = _ExpertsStruct(*[_ptr(t) for t in self.tensors])
+        self._ref = ctypes.addressof(self._struct)
+
+
+def moe_quantize_fp8(X, Q, scale, layout, stream=None):
+    """X (bf16 or fp32, [rows][cols] or [n][rows][cols]) to codes Q (float8_e4m3fn, X's shape) and fp32 scales:
+    layout "rows": one for each 128 columns of a row, [..][rows][ceil(cols/128)]; "blocks": one for each 128 x 128
+    block, [..][ceil(rows/128)][ceil(cols/128)]."""
+    if isinstance(layout, str):
+        if layout not in FP8_LAYOUTS:
+            raise ValueError("layout %r: one of %s expected" % (layout, sorted(FP8_LAYOUTS)))
+        layout = FP8_LAYOUTS[layout]
+    device = _device_of("X", X)
+    shape = tuple(X.shape)
+    if len(shape) not in (2, 3):
+        raise ValueError("X: [rows][cols] or [n][rows][cols] expected, got shape %s" % (shape,))
+    lead, (rows, cols) = shape[:-2], shape[-2:]
+    dt = _dt(X)
+    x = _on("X", X, shape, X.dtype, device)
+    q = _on("Q", Q, shape, torch.float8_e4m3fn, device)
+    s = _on("scale", scale, lead + (_groups(rows) if layout == FP8_BLOCKS else rows, _groups(cols)), torch.float32, device)
+    _call(device, lib.moe_quantize_fp8, stream, layout, dt, lead[0] if lead else 1, rows, cols, x, q, s)
+
+
+def skinny_gemm_fp8(X, W, Y, x_scale=None, R=None, ws=None, stream=None):
+    """Y = X . W^T (+ R) over an Fp8Weight.  X [B][K]: bf16, or float8_e4m3fn with x_scale fp32
+    [B][ceil(K/128)]; Y [B][N] bf16 or fp32, R [B][N] bf16."""
+    if not isinstance(W, Fp8Weight):
+        raise TypeError("W: an Fp8Weight expected, got %s" % type(W).__name__)
+    device, N, K = W.device, W.N, W.K
+    B, _ = _shape("X", X, 2)
+    if X.dtype == torch.float8_e4m3fn:
+        xdt, x = DT_E4M3, _on("X", X, (B, K), torch.float8_e4m3fn, device)
+        xs = _on("x_scale", x_scale, (B, _groups(K)), torch.float32, device)
+    else:
+        if x_scale is not None:
+            raise ValueError("x_scale belongs to float8_e4m3fn activations")
+        xdt, xs, x = DT_BF16, None, _on("X", X, (B, K), torch.bfloat16, device)
+    r = None if R is None else _on("R", R, (B, N), torch.bfloat16, device)
+    _shape("Y", Y, 2)
+    ydt = DT_F32 if Y.dtype == torch.float32 else DT_BF16
+    y = _on("Y", Y, (B, N), torch.float32 if ydt == DT_F32 else torch.bfloat16, device)
+    wp, wn = _ws(ws, device)
+    _call(device, lib.skinny_gemm_fp8, stream, xdt, B, N, K, x, xs, W._ptrs[0], W._ptrs[1], r, y, ydt, wp, wn)
+
+
+def _ws(ws, device):
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.dim() != 1:
+        raise TypeError("ws: a 1-D uint8 torch.Tensor expected")
+    n = ws.numel()
+    return _on("ws", ws, (n,), torch.uint8, device), n
+
+
+def moe_block_fp8(X, Wr, k, experts, out, ws, bias=None, bias_ld=0, topk_ids=None, topk_w=None, stream=None):
+    """moe_block over Fp8Experts: X [B][d], Wr [E][d] and out [B][d] bf16."""
+    if not isinstance(experts, Fp8Experts):
+        raise TypeError("experts: an Fp8Experts expected, got %s" % type(experts).__name__)
+    device, E, d, I, Is = experts.device, experts.E, experts.d, experts.I, experts.Is
+    B, _ = _shape("X", X, 2)
+    x = _on("X", X, (B, d), torch.bfloat16, device)
+    wr = _on("Wr", Wr, (E, d), torch.bfloat16, device)
+    b = None
+    if bias is not None:
+        if bias_ld not in (0, E):
+            raise ValueError("bias_ld must be 0 (bias [E]) or E (bias [B][E]), got %d" % bias_ld)
+        b = _on("bias", bias, (B, E) if bias_ld else (E,), torch.float32, device)
+    o = _on("out", out, (B, d), torch.bfloat16, device)
+    ids = None if topk_ids is None else _on("topk_ids", topk_ids, (B, k), torch.int32, device)
+    w = None if topk_w is None else _on("topk_w", topk_w, (B, k), torch.float32, device)
+    if ws is None:
+        raise ValueError("ws is required")
+    wp, wn = _ws(ws, device)
+    _call(device, lib.moe_block_fp8, stream, DT_BF16, B, d, E, k, I, Is, x, wr, b, bias_ld, experts._ref, o, ids, w,
+          wp, wn)

@@ -17,6 +17,7 @@
 #include <cstring>
 
 #include "expert_core.hpp"
+#include "fp8.hpp"
 #include "internal.hpp"
 #include "moe_skinny.h"
 
@@ -279,6 +280,30 @@ BlockWs block_ws(int bf16, int B, int d, int E, int k, int I, int Is) {
   return b;
 }
 
+// Block over 8-bit weights: the router's layout at offset 0, then h, ids,
+// weights, plan and the per-token selection's ready words.
+struct BlockFp8Ws {
+  size_t h, ids, w, plan, ready, total;
+  int hld;
+};
+
+BlockFp8Ws block_fp8_ws(int B, int d, int E, int k, int I, int Is) {
+  BlockFp8Ws b;
+  b.hld = I > Is ? I : Is;
+  size_t o = up(skinny_ws(B, E, d, 1, true).total);
+  b.h = o;
+  o = up(o + (size_t)(B * k + B) * b.hld * 4);
+  b.ids = o;
+  o = up(o + (size_t)B * k * 4);
+  b.w = o;
+  o = up(o + (size_t)B * k * 4);
+  b.plan = o;
+  o = up(o + (size_t)moe_plan_words(B, k, E) * 4);
+  b.ready = o;
+  b.total = up(o + (size_t)B * k * 4);
+  return b;
+}
+
 // ---- validation -----------------------------------------------------------
 
 moe_status_t check_dtype(int dt) {
@@ -503,6 +528,11 @@ size_t moe_workspace_bytes(int op, int dtype, int B, int d, int E, int k, int I,
     case MOE_OP_ROUTE_LATENT:   // N = L, the latent rows
       if (E <= 0 || d <= 0 || N <= 0) return 0;
       return skinny_ws(B, E + N, d, bf16, true).total;
+    case MOE_OP_SKINNY_GEMM_FP8:
+      return 0;
+    case MOE_OP_BLOCK_FP8:
+      if (E <= 0 || d <= 0 || k <= 0) return 0;
+      return block_fp8_ws(B, d, E, k, I, Is).total;
   }
   return 0;
 }
@@ -975,6 +1005,179 @@ moe_status_t moe_block_noalloc(int dtype, int B, int d, int E, int k, int I, int
   // captured in a graph)
   if ((s = hip_status(launch_fill_zero(w, kHeaderBytes, st), "scratch header"))) return s;
   return block_run(a, v, force, L, w, st);
+}
+
+}  // extern "C"
+
+// ---- 8-bit weights ------------------------------------------------------------
+
+namespace {
+
+constexpr int kMaxK8 = 65536;        // columns of an 8-bit product: byte offsets within 64 rows stay below 2^31
+constexpr int kMaxN8 = 1 << 24;
+
+moe_status_t block_fp8_run(int B, int d, int E, int k, int I, int Is, const void* X, const void* Wr, const float* bias,
+                           int bias_ld, const moe_fp8_experts_t& W, void* out, int32_t* topk_ids, float* topk_w,
+                           int v, char* w, hipStream_t st) {
+  const bool shared = W.Ws13 != nullptr;
+  const BlockFp8Ws L = block_fp8_ws(B, d, E, k, I, shared ? Is : 0);
+  const int sched = schedule();
+  if (sched == MOE_SCHEDULE_FUSED)
+    return fail(MOE_EUNSUPPORTED, "the fused block kernel has no 8-bit weights");
+  int32_t* ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(w + L.ids);
+  float* tw = topk_w ? topk_w : reinterpret_cast<float*>(w + L.w);
+  int32_t* plan = reinterpret_cast<int32_t*>(w + L.plan);
+  Fp8ExpertLaunch a = {};
+  ExpertLaunch& ex = a.e;
+  ex = expert_launch(MOE_DT_BF16, B, d, E, k, I, X, plan, W.W13, W.W2, Is, W.Ws13, W.Ws2, nullptr, VAR_AUTO);
+  ex.h = reinterpret_cast<float*>(w + L.h);
+  ex.hld = L.hld;
+  ex.topk_w = tw;
+  ex.out = out;
+  ex.out_bf16 = 1;
+  a.s13 = W.s13;
+  a.s2 = W.s2;
+  a.ss13 = W.ss13;
+  a.ss2 = W.ss2;
+  char d1[200] = "", d2[128] = "", d3[128] = "";
+  moe_status_t s;
+  // The schedules of moe_block: at B * k <= 64 on a vector router the gate/up
+  // launch selects the tokens' experts (and at B <= 2 scores the router rows
+  // too); otherwise the router's finish does, and after the matrix router
+  // every gate/up workgroup builds the plan from the ids.
+  if (v != VAR_MFMA && B <= 8 && B * k <= 64) {
+    ex.ids_out = ids;
+    ex.w_out = tw;
+    ex.plan_out = plan;
+    ex.status = reinterpret_cast<uint32_t*>(w + moe_workspace_status_offset());
+    ex.spin_limit = 1 << 20;   // about a second of polling
+    if (B <= kKeysMaxB && sched != MOE_SCHEDULE_LAUNCHES) {
+      ex.Wr = Wr;
+      ex.rbias = bias;
+      ex.rbias_ld = bias_ld;
+      ex.router_wgs = (E + kRouterRowsInUp - 1) / kRouterRowsInUp;
+      ex.lkeys = reinterpret_cast<uint32_t*>(w + kKeysOff);
+      snprintf(d1, sizeof d1, "rows in the gate/up launch, %d workgroups", ex.router_wgs);
+    } else {
+      if (B >= 2) ex.ready = reinterpret_cast<int32_t*>(w + L.ready);
+      if ((s = run_route(MOE_DT_BF16, B, d, E, k, X, Wr, bias, bias_ld, ids, tw, plan, nullptr, w, st, d1, sizeof d1,
+                         nullptr, 0, &ex.logits, 0, ex.ready, ex.ready ? B * k : 0)))
+        return s;
+    }
+  } else {
+    const bool consumer_plan = v == VAR_MFMA && B > 8;
+    if (consumer_plan) {
+      ex.ids_in = ids;
+      ex.plan_out = plan;
+    }
+    if ((s = run_route(MOE_DT_BF16, B, d, E, k, X, Wr, bias, bias_ld, ids, tw, plan, nullptr, w, st, d1, sizeof d1,
+                       nullptr, 1, nullptr, consumer_plan ? 1 : 0)))
+      return s;
+  }
+  if ((s = hip_status(launch_expert_up_fp8(a, st, d2, sizeof d2), "expert gate/up launch"))) return s;
+  ex.ids_in = nullptr;   // the down launch reads the plan the gate/up launch stored
+  if ((s = hip_status(launch_expert_down_combine_fp8(a, st, d3, sizeof d3), "expert down+combine launch"))) return s;
+  char desc[480];
+  snprintf(desc, sizeof desc, "route[%s] %s; %s", d1, d2, d3);
+  record("moe_block_fp8", B, desc);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_quantize_fp8(int layout, int dtype, int n, int rows, int cols, const void* X, void* Q, float* scale,
+                              void* stream) {
+  g_err[0] = 0;
+  moe_status_t s = check_dtype(dtype);
+  if (s) return s;
+  if (layout != MOE_FP8_ROWS && layout != MOE_FP8_BLOCKS) return fail(MOE_EINVAL, "unknown layout %d", layout);
+  if (n <= 0 || rows <= 0 || cols <= 0) return fail(MOE_EINVAL, "non-positive size");
+  if (!aligned(X) || !aligned(Q) || !aligned(scale)) return fail(MOE_EINVAL, "X, Q or scale null or not 16-byte aligned");
+  if (cols % 16) return fail(MOE_EUNSUPPORTED, "cols=%d not a multiple of 16", cols);
+  // groups: 31 bits in the row layout (8 threads each, in a bounded grid), a
+  // workgroup of 256 threads each in the block layout (32 bits of threads)
+  const size_t KB = ((size_t)cols + 127) / 128, RB = layout == MOE_FP8_BLOCKS ? ((size_t)rows + 127) / 128 : (size_t)rows;
+  const size_t most = layout == MOE_FP8_BLOCKS ? ((size_t)1 << 24) - 1 : (size_t)0x7fffffff;
+  if ((size_t)n * RB > most || (size_t)n * RB * KB > most)
+    return fail(MOE_EUNSUPPORTED, "%d x %d x %d: more than %zu scales", n, rows, cols, most);
+  QuantizeLaunch a = {};
+  a.bf16 = dtype == MOE_DT_BF16;
+  a.blocks = layout == MOE_FP8_BLOCKS;
+  a.n = n;
+  a.rows = rows;
+  a.cols = cols;
+  a.X = X;
+  a.Q = static_cast<uint8_t*>(Q);
+  a.scale = scale;
+  s = hip_status(launch_quantize(a, reinterpret_cast<hipStream_t>(stream)), "moe_quantize_fp8 launch");
+  if (!s) record("moe_quantize_fp8", rows, a.blocks ? "blocks" : "rows");
+  return s;
+}
+
+moe_status_t skinny_gemm_fp8(int x_dtype, int B, int N, int K, const void* X, const float* x_scale, const void* W,
+                             const float* w_scale, const void* R, void* Y, int y_dtype, void* ws, size_t ws_bytes,
+                             void* stream) {
+  g_err[0] = 0;
+  if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_E4M3) return fail(MOE_EINVAL, "x_dtype %d", x_dtype);
+  if (y_dtype != MOE_DT_BF16 && y_dtype != MOE_DT_F32) return fail(MOE_EINVAL, "y_dtype %d", y_dtype);
+  if (B <= 0 || N <= 0 || K <= 0) return fail(MOE_EINVAL, "non-positive size");
+  if (!aligned(X) || !aligned(W) || !aligned(w_scale) || !aligned(Y))
+    return fail(MOE_EINVAL, "X, W, w_scale or Y null or not 16-byte aligned");
+  if (x_dtype == MOE_DT_E4M3 && !aligned(x_scale)) return fail(MOE_EINVAL, "x_scale null or not 16-byte aligned");
+  if (x_dtype == MOE_DT_BF16 && x_scale) return fail(MOE_EINVAL, "bf16 activations have no x_scale");
+  if (R && !aligned(R)) return fail(MOE_EINVAL, "R not 16-byte aligned");
+  if (B > kMaxB) return fail(MOE_EUNSUPPORTED, "B=%d outside 1..%d", B, kMaxB);
+  if (K % 16 || K > kMaxK8) return fail(MOE_EUNSUPPORTED, "K=%d must be a multiple of 16 up to %d", K, kMaxK8);
+  if (N > kMaxN8) return fail(MOE_EUNSUPPORTED, "N=%d > %d", N, kMaxN8);
+  GemmFp8Launch a = {};
+  a.x_e4m3 = x_dtype == MOE_DT_E4M3;
+  a.X = X;
+  a.Xs = x_scale;
+  a.W = static_cast<const uint8_t*>(W);
+  a.Ws = w_scale;
+  a.R = static_cast<const uint16_t*>(R);
+  a.Y = Y;
+  a.y_bf16 = y_dtype == MOE_DT_BF16;
+  a.M = B;
+  a.N = N;
+  a.K = K;
+  char desc[160];
+  const moe_status_t s = hip_status(launch_gemm_fp8(a, reinterpret_cast<hipStream_t>(stream), desc, sizeof desc),
+                                    "skinny_gemm_fp8 launch");
+  if (!s) record("skinny_gemm_fp8", B, desc);
+  return s;
+}
+
+moe_status_t moe_block_fp8(int dtype, int B, int d, int E, int k, int I, int Is, const void* X, const void* Wr,
+                           const float* bias, int bias_ld, const moe_fp8_experts_t* experts, void* out,
+                           int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status_t s = check_route_dims(dtype, B, d, E, k);
+  if (s) return s;
+  if (dtype != MOE_DT_BF16) return fail(MOE_EUNSUPPORTED, "8-bit experts take bf16 activations");
+  if (d > kMaxK8) return fail(MOE_EUNSUPPORTED, "d=%d > %d", d, kMaxK8);
+  if (!experts) return fail(MOE_EINVAL, "experts null");
+  const moe_fp8_experts_t& W = *experts;
+  if ((s = check_inter(dtype, I, "I"))) return s;
+  if (W.Ws13 && (s = check_inter(dtype, Is, "Is"))) return s;
+  if (!aligned(X) || !aligned(Wr) || !aligned(out)) return fail(MOE_EINVAL, "X, Wr or out null or misaligned");
+  if (!aligned(W.W13) || !aligned(W.s13) || !aligned(W.W2) || !aligned(W.s2))
+    return fail(MOE_EINVAL, "W13, s13, W2 or s2 null or misaligned");
+  if (W.Ws13 && (!aligned(W.Ws13) || !aligned(W.ss13) || !aligned(W.Ws2) || !aligned(W.ss2)))
+    return fail(MOE_EINVAL, "Ws13, ss13, Ws2 or ss2 null or misaligned");
+  if (bias && !aligned(bias)) return fail(MOE_EINVAL, "bias misaligned");
+  if (bias && bias_ld != 0 && bias_ld != E) return fail(MOE_EINVAL, "bias_ld must be 0 or E");
+  if ((topk_ids && !aligned(topk_ids)) || (topk_w && !aligned(topk_w)))
+    return fail(MOE_EINVAL, "topk_ids or topk_w misaligned");
+  int v;
+  if ((s = resolve_skinny(1, B, d, &v))) return s;
+  const size_t need = block_fp8_ws(B, d, E, k, I, W.Ws13 ? Is : 0).total;
+  if (!aligned(ws)) return fail(MOE_EINVAL, "ws null or misaligned");
+  if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  return block_fp8_run(B, d, E, k, I, Is, X, Wr, bias, bias_ld, W, out, topk_ids, topk_w, v, static_cast<char*>(ws),
+                       reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"
