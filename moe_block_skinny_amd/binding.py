@@ -460,41 +460,48 @@ def _groups(n):
     return (n + FP8_BLOCK - 1) // FP8_BLOCK
 
 
-def _on(name, t, shape, dtype, device):
-    """The checks of _Args.arr and on_gpu for one tensor of a call whose device is known."""
-    if not isinstance(t, torch.Tensor):
-        if t is None:
-            raise ValueError("%s is required" % name)
+def _on(name, t, shape, dtype, index):
+    """The checks of _Args.arr and on_gpu for one tensor of a call on GPU `index` (-1: host memory, refused
+    later); its address.  One condition for what passes: the checks are most of a small call's host time."""
+    if isinstance(t, torch.Tensor):
+        if t.shape == shape and t.dtype == dtype and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    elif t is None:
+        raise ValueError("%s is required" % name)
+    else:
         raise TypeError("%s: a torch.Tensor expected, got %s" % (name, type(t).__name__))
     if t.shape != shape:
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.device != device:
-        if t.device.type != "cuda":
-            raise ValueError("%s must be in GPU memory (device %s)" % (name, t.device))
-        raise ValueError("%s is on %s, the other arguments on %s" % (name, t.device, device))
-    return t.data_ptr()
+    if t.device.type != "cuda":
+        raise ValueError("%s must be in GPU memory (device %s)" % (name, t.device))
+    raise ValueError("%s is on %s, the other arguments on GPU %d" % (name, t.device, index))
 
 
-def _device_of(name, t):
+def _index_of(name, t):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: a torch.Tensor expected, got %s" % (name, type(t).__name__))
-    return t.device
+    return t.get_device()
 
 
-def _call(device, f, stream, *args):
-    """f(*args, stream) with `device` current: a launch goes to the current device, and without a stream to the
+_raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream() builds an object: 3 us of a 6 us call
+
+
+def _call(index, f, stream, *args):
+    """f(*args, stream) with GPU `index` current: a launch goes to the current device, and without a stream to the
     stream that is current there."""
-    if device.type != "cuda":
-        raise ValueError("the arguments must be in GPU memory (device %s)" % device)
-    if torch.cuda.current_device() == device.index:
-        _check(f(*args, _stream(stream)))
+    if index < 0:
+        raise ValueError("the arguments must be in GPU memory")
+    if torch.cuda.current_device() == index:
+        s = f(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
-            _check(f(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            s = f(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if s != OK:
+        _check(s)
 
 
 class Fp8Weight:
@@ -503,7 +510,7 @@ class Fp8Weight:
 
     def __init__(self, codes, scale):
         self.N, self.K = _shape("codes", codes, 2)
-        self.device = codes.device
+        self.index = codes.get_device()
         a = _Args()
         a.arr("codes", codes, (self.N, self.K), torch.float8_e4m3fn)
         a.arr("scale", scale, (_groups(self.N), _groups(self.K)), torch.float32)
@@ -527,7 +534,7 @@ class Fp8Experts:
         if two_i % 2:
             raise ValueError("W13: [E][2I][d] expected, got %s" % (tuple(W13.shape),))
         E, d, I = self.E, self.d, two_i // 2
-        self.I, self.Is, self.device = I, 0, W13.device
+        self.I, self.Is, self.index = I, 0, W13.get_device()
         f8, f32 = torch.float8_e4m3fn, torch.float32
         a = _Args()
         a.arr("W13", W13, (E, 2 * I, d), f8)
@@ -560,16 +567,16 @@ def moe_quantize_fp8(X, Q, scale, layout, stream=None):
         if layout not in FP8_LAYOUTS:
             raise ValueError("layout %r: one of %s expected" % (layout, sorted(FP8_LAYOUTS)))
         layout = FP8_LAYOUTS[layout]
-    device = _device_of("X", X)
-    shape = tuple(X.shape)
+    index = _index_of("X", X)
+    shape = X.shape
     if len(shape) not in (2, 3):
-        raise ValueError("X: [rows][cols] or [n][rows][cols] expected, got shape %s" % (shape,))
+        raise ValueError("X: [rows][cols] or [n][rows][cols] expected, got shape %s" % (tuple(shape),))
     lead, (rows, cols) = shape[:-2], shape[-2:]
     dt = _dt(X)
-    x = _on("X", X, shape, X.dtype, device)
-    q = _on("Q", Q, shape, torch.float8_e4m3fn, device)
-    s = _on("scale", scale, lead + (_groups(rows) if layout == FP8_BLOCKS else rows, _groups(cols)), torch.float32, device)
-    _call(device, lib.moe_quantize_fp8, stream, layout, dt, lead[0] if lead else 1, rows, cols, x, q, s)
+    x = _on("X", X, shape, X.dtype, index)
+    q = _on("Q", Q, shape, torch.float8_e4m3fn, index)
+    s = _on("scale", scale, lead + (_groups(rows) if layout == FP8_BLOCKS else rows, _groups(cols)), torch.float32, index)
+    _call(index, lib.moe_quantize_fp8, stream, layout, dt, lead[0] if lead else 1, rows, cols, x, q, s)
 
 
 def skinny_gemm_fp8(X, W, Y, x_scale=None, R=None, ws=None, stream=None):
@@ -577,50 +584,57 @@ def skinny_gemm_fp8(X, W, Y, x_scale=None, R=None, ws=None, stream=None):
     [B][ceil(K/128)]; Y [B][N] bf16 or fp32, R [B][N] bf16."""
     if not isinstance(W, Fp8Weight):
         raise TypeError("W: an Fp8Weight expected, got %s" % type(W).__name__)
-    device, N, K = W.device, W.N, W.K
-    B, _ = _shape("X", X, 2)
+    index, N, K = W.index, W.N, W.K
+    B = _rows(X)
     if X.dtype == torch.float8_e4m3fn:
-        xdt, x = DT_E4M3, _on("X", X, (B, K), torch.float8_e4m3fn, device)
-        xs = _on("x_scale", x_scale, (B, _groups(K)), torch.float32, device)
+        xdt, x = DT_E4M3, _on("X", X, (B, K), torch.float8_e4m3fn, index)
+        xs = _on("x_scale", x_scale, (B, _groups(K)), torch.float32, index)
     else:
         if x_scale is not None:
             raise ValueError("x_scale belongs to float8_e4m3fn activations")
-        xdt, xs, x = DT_BF16, None, _on("X", X, (B, K), torch.bfloat16, device)
-    r = None if R is None else _on("R", R, (B, N), torch.bfloat16, device)
-    _shape("Y", Y, 2)
-    ydt = DT_F32 if Y.dtype == torch.float32 else DT_BF16
-    y = _on("Y", Y, (B, N), torch.float32 if ydt == DT_F32 else torch.bfloat16, device)
-    wp, wn = _ws(ws, device)
-    _call(device, lib.skinny_gemm_fp8, stream, xdt, B, N, K, x, xs, W._ptrs[0], W._ptrs[1], r, y, ydt, wp, wn)
+        xdt, xs, x = DT_BF16, None, _on("X", X, (B, K), torch.bfloat16, index)
+    r = None if R is None else _on("R", R, (B, N), torch.bfloat16, index)
+    ydt = DT_F32 if getattr(Y, "dtype", None) == torch.float32 else DT_BF16
+    y = _on("Y", Y, (B, N), torch.float32 if ydt == DT_F32 else torch.bfloat16, index)
+    wp, wn = _ws(ws, index)
+    _call(index, lib.skinny_gemm_fp8, stream, xdt, B, N, K, x, xs, W._ptrs[0], W._ptrs[1], r, y, ydt, wp, wn)
 
 
-def _ws(ws, device):
+def _ws(ws, index):
     if ws is None:
         return None, 0
     if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.dim() != 1:
         raise TypeError("ws: a 1-D uint8 torch.Tensor expected")
-    n = ws.numel()
-    return _on("ws", ws, (n,), torch.uint8, device), n
+    return _on("ws", ws, ws.shape, torch.uint8, index), ws.shape[0]
+
+
+def _rows(X):
+    """B of X [B][..]: the other checks follow."""
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X: a torch.Tensor expected, got %s" % type(X).__name__)
+    if X.dim() != 2:
+        raise ValueError("X: 2 dimensions expected, got shape %s" % (tuple(X.shape),))
+    return X.shape[0]
 
 
 def moe_block_fp8(X, Wr, k, experts, out, ws, bias=None, bias_ld=0, topk_ids=None, topk_w=None, stream=None):
     """moe_block over Fp8Experts: X [B][d], Wr [E][d] and out [B][d] bf16."""
     if not isinstance(experts, Fp8Experts):
         raise TypeError("experts: an Fp8Experts expected, got %s" % type(experts).__name__)
-    device, E, d, I, Is = experts.device, experts.E, experts.d, experts.I, experts.Is
-    B, _ = _shape("X", X, 2)
-    x = _on("X", X, (B, d), torch.bfloat16, device)
-    wr = _on("Wr", Wr, (E, d), torch.bfloat16, device)
+    index, E, d, I, Is = experts.index, experts.E, experts.d, experts.I, experts.Is
+    B = _rows(X)
+    x = _on("X", X, (B, d), torch.bfloat16, index)
+    wr = _on("Wr", Wr, (E, d), torch.bfloat16, index)
     b = None
     if bias is not None:
         if bias_ld not in (0, E):
             raise ValueError("bias_ld must be 0 (bias [E]) or E (bias [B][E]), got %d" % bias_ld)
-        b = _on("bias", bias, (B, E) if bias_ld else (E,), torch.float32, device)
-    o = _on("out", out, (B, d), torch.bfloat16, device)
-    ids = None if topk_ids is None else _on("topk_ids", topk_ids, (B, k), torch.int32, device)
-    w = None if topk_w is None else _on("topk_w", topk_w, (B, k), torch.float32, device)
+        b = _on("bias", bias, (B, E) if bias_ld else (E,), torch.float32, index)
+    o = _on("out", out, (B, d), torch.bfloat16, index)
+    ids = None if topk_ids is None else _on("topk_ids", topk_ids, (B, k), torch.int32, index)
+    w = None if topk_w is None else _on("topk_w", topk_w, (B, k), torch.float32, index)
     if ws is None:
         raise ValueError("ws is required")
-    wp, wn = _ws(ws, device)
-    _call(device, lib.moe_block_fp8, stream, DT_BF16, B, d, E, k, I, Is, x, wr, b, bias_ld, experts._ref, o, ids, w,
+    wp, wn = _ws(ws, index)
+    _call(index, lib.moe_block_fp8, stream, DT_BF16, B, d, E, k, I, Is, x, wr, b, bias_ld, experts._ref, o, ids, w,
           wp, wn)

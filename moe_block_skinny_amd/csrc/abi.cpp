@@ -27,6 +27,13 @@ namespace {
 
 thread_local char g_err[512] = "";
 thread_local char g_variant[256] = "";
+// The 8-bit calls describe the shape they took only when asked for it
+// (moe_last_variant, MOE_TRACE): writing the text took longer than the rest of
+// a small call's host work.
+thread_local struct {
+  void (*write)(const int* v, char* to, size_t len) = nullptr;   // null: g_variant holds the text
+  int v[16];
+} g_shape;
 std::atomic<int> g_force{-1};  // -1: not yet read from the environment
 std::atomic<int> g_sched{-1};  // block schedule; -1: not yet read from the environment
 std::atomic<int> g_shared{-1}; // where the shared expert's gate/up runs; -1: not yet read
@@ -115,7 +122,23 @@ bool trace_on() {
   return on != 0;
 }
 
+void write_shape() {
+  if (!g_shape.write) return;
+  g_shape.write(g_shape.v, g_variant, sizeof g_variant);
+  g_shape.write = nullptr;
+}
+
+void record_shape(void (*write)(const int*, char*, size_t), const int* v, int n) {
+  g_shape.write = write;
+  memcpy(g_shape.v, v, n * sizeof(int));
+  if (trace_on()) {
+    write_shape();
+    fprintf(stderr, "[moe_skinny] %s\n", g_variant);
+  }
+}
+
 void record(const char* op, int B, const char* desc) {
+  g_shape.write = nullptr;
   snprintf(g_variant, sizeof g_variant, "%s B=%d %s", op, B, desc);
   if (trace_on()) fprintf(stderr, "[moe_skinny] %s\n", g_variant);
 }
@@ -280,19 +303,36 @@ BlockWs block_ws(int bf16, int B, int d, int E, int k, int I, int Is) {
   return b;
 }
 
+// Dense product over 8-bit weights: after the header, the K slices' sums.
+// The row groups' arrival counters are the header's words from 32 on: with
+// more than one slice there are at most 128 of them.
+size_t gemm_fp8_ws(int B, int N, int K) {
+  const size_t part = gemm_fp8_plan(B, N, K).part_bytes;
+  return part ? up(kHeaderBytes + part) : 0;
+}
+
 // Block over 8-bit weights: the router's layout at offset 0, then h, ids,
 // weights, plan and the per-token selection's ready words.
+// h: B <= 8 slot rows of fp32's bytes (two bf16 planes); beyond, two planes of
+// 16-token tiles with rows padded to whole scale blocks.
 struct BlockFp8Ws {
-  size_t h, ids, w, plan, ready, total;
+  size_t h, h_lo, ids, w, plan, ready, total;
   int hld;
 };
 
 BlockFp8Ws block_fp8_ws(int B, int d, int E, int k, int I, int Is) {
   BlockFp8Ws b;
   b.hld = I > Is ? I : Is;
+  if (B > 8) b.hld = (b.hld + 127) / 128 * 128;
   size_t o = up(skinny_ws(B, E, d, 1, true).total);
   b.h = o;
-  o = up(o + (size_t)(B * k + B) * b.hld * 4);
+  b.h_lo = 0;
+  if (B > 8) {
+    b.h_lo = o = up(o + (size_t)ht_rows(B, k, E) * b.hld * 2);
+    o = up(o + (size_t)ht_rows(B, k, E) * b.hld * 2);
+  } else {
+    o = up(o + (size_t)(B * k + B) * b.hld * 4);
+  }
   b.ids = o;
   o = up(o + (size_t)B * k * 4);
   b.w = o;
@@ -481,7 +521,10 @@ moe_status_t moe_profile_events(int kernel, void* start_event, void* stop_event)
   g_prof.stop = reinterpret_cast<hipEvent_t>(stop_event);
   return MOE_OK;
 }
-const char* moe_last_variant(void) { return g_variant; }
+const char* moe_last_variant(void) {
+  write_shape();
+  return g_variant;
+}
 
 int moe_set_variant(int variant) {
   const int prev = forced();
@@ -529,7 +572,8 @@ size_t moe_workspace_bytes(int op, int dtype, int B, int d, int E, int k, int I,
       if (E <= 0 || d <= 0 || N <= 0) return 0;
       return skinny_ws(B, E + N, d, bf16, true).total;
     case MOE_OP_SKINNY_GEMM_FP8:
-      return 0;
+      if (N <= 0 || K <= 0) return 0;
+      return gemm_fp8_ws(B, N, K);
     case MOE_OP_BLOCK_FP8:
       if (E <= 0 || d <= 0 || k <= 0) return 0;
       return block_fp8_ws(B, d, E, k, I, Is).total;
@@ -1032,6 +1076,10 @@ moe_status_t block_fp8_run(int B, int d, int E, int k, int I, int Is, const void
   ex = expert_launch(MOE_DT_BF16, B, d, E, k, I, X, plan, W.W13, W.W2, Is, W.Ws13, W.Ws2, nullptr, VAR_AUTO);
   ex.h = reinterpret_cast<float*>(w + L.h);
   ex.hld = L.hld;
+  if (L.h_lo) {
+    ex.ht_hi = reinterpret_cast<uint16_t*>(w + L.h);
+    ex.ht_lo = reinterpret_cast<uint16_t*>(w + L.h_lo);
+  }
   ex.topk_w = tw;
   ex.out = out;
   ex.out_bf16 = 1;
@@ -1039,7 +1087,7 @@ moe_status_t block_fp8_run(int B, int d, int E, int k, int I, int Is, const void
   a.s2 = W.s2;
   a.ss13 = W.ss13;
   a.ss2 = W.ss2;
-  char d1[200] = "", d2[128] = "", d3[128] = "";
+  Fp8Shape up, down;
   moe_status_t s;
   // The schedules of moe_block: at B * k <= 64 on a vector router the gate/up
   // launch selects the tokens' experts (and at B <= 2 scores the router rows
@@ -1057,10 +1105,9 @@ moe_status_t block_fp8_run(int B, int d, int E, int k, int I, int Is, const void
       ex.rbias_ld = bias_ld;
       ex.router_wgs = (E + kRouterRowsInUp - 1) / kRouterRowsInUp;
       ex.lkeys = reinterpret_cast<uint32_t*>(w + kKeysOff);
-      snprintf(d1, sizeof d1, "rows in the gate/up launch, %d workgroups", ex.router_wgs);
     } else {
       if (B >= 2) ex.ready = reinterpret_cast<int32_t*>(w + L.ready);
-      if ((s = run_route(MOE_DT_BF16, B, d, E, k, X, Wr, bias, bias_ld, ids, tw, plan, nullptr, w, st, d1, sizeof d1,
+      if ((s = run_route(MOE_DT_BF16, B, d, E, k, X, Wr, bias, bias_ld, ids, tw, plan, nullptr, w, st, nullptr, 0,
                          nullptr, 0, &ex.logits, 0, ex.ready, ex.ready ? B * k : 0)))
         return s;
     }
@@ -1070,16 +1117,19 @@ moe_status_t block_fp8_run(int B, int d, int E, int k, int I, int Is, const void
       ex.ids_in = ids;
       ex.plan_out = plan;
     }
-    if ((s = run_route(MOE_DT_BF16, B, d, E, k, X, Wr, bias, bias_ld, ids, tw, plan, nullptr, w, st, d1, sizeof d1,
+    if ((s = run_route(MOE_DT_BF16, B, d, E, k, X, Wr, bias, bias_ld, ids, tw, plan, nullptr, w, st, nullptr, 0,
                        nullptr, 1, nullptr, consumer_plan ? 1 : 0)))
       return s;
   }
-  if ((s = hip_status(launch_expert_up_fp8(a, st, d2, sizeof d2), "expert gate/up launch"))) return s;
+  if ((s = hip_status(launch_expert_up_fp8(a, st, &up), "expert gate/up launch"))) return s;
   ex.ids_in = nullptr;   // the down launch reads the plan the gate/up launch stored
-  if ((s = hip_status(launch_expert_down_combine_fp8(a, st, d3, sizeof d3), "expert down+combine launch"))) return s;
-  char desc[480];
-  snprintf(desc, sizeof desc, "route[%s] %s; %s", d1, d2, d3);
-  record("moe_block_fp8", B, desc);
+  if ((s = hip_status(launch_expert_down_combine_fp8(a, st, &down), "expert down+combine launch"))) return s;
+  const int v8[9] = {B, v, ex.router_wgs, up.grid, up.waves, ex.logits != nullptr, down.grid, down.rows, down.waves};
+  record_shape([](const int* v, char* to, size_t len) {
+    const char* names[] = {"auto", "gemv", "splitk", "mfma", "rows"};
+    snprintf(to, len, "moe_block_fp8 B=%d route[%s%s] up grid=%d waves/wg=%d%s; down+combine grid=%d rows/wg=%d waves/wg=%d", v[0],
+             v[2] ? "rows in the gate/up launch, " : "", names[v[1]], v[3], v[4], v[5] || v[2] ? " +top-k/plan" : "", v[6], v[7], v[8]);
+  }, v8, 9);
   return MOE_OK;
 }
 
@@ -1112,7 +1162,12 @@ moe_status_t moe_quantize_fp8(int layout, int dtype, int n, int rows, int cols, 
   a.Q = static_cast<uint8_t*>(Q);
   a.scale = scale;
   s = hip_status(launch_quantize(a, reinterpret_cast<hipStream_t>(stream)), "moe_quantize_fp8 launch");
-  if (!s) record("moe_quantize_fp8", rows, a.blocks ? "blocks" : "rows");
+  if (!s) {
+    const int v[4] = {n, rows, cols, a.blocks};
+    record_shape([](const int* v, char* to, size_t len) {
+      snprintf(to, len, "moe_quantize_fp8 %s n=%d rows=%d cols=%d", v[3] ? "blocks" : "rows", v[0], v[1], v[2]);
+    }, v, 4);
+  }
   return s;
 }
 
@@ -1143,10 +1198,23 @@ moe_status_t skinny_gemm_fp8(int x_dtype, int B, int N, int K, const void* X, co
   a.M = B;
   a.N = N;
   a.K = K;
-  char desc[160];
-  const moe_status_t s = hip_status(launch_gemm_fp8(a, reinterpret_cast<hipStream_t>(stream), desc, sizeof desc),
+  const size_t need = gemm_fp8_ws(B, N, K);
+  if (need && !aligned(ws)) return fail(MOE_EINVAL, "ws null or misaligned");
+  if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  if (need) {
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes);
+    a.counter = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + 32 * 4);
+  }
+  Fp8Shape shape;
+  const moe_status_t s = hip_status(launch_gemm_fp8(a, reinterpret_cast<hipStream_t>(stream), &shape),
                                     "skinny_gemm_fp8 launch");
-  if (!s) record("skinny_gemm_fp8", B, desc);
+  if (!s) {
+    const int v[9] = {a.x_e4m3, B, N, K, shape.rows, shape.tokens, shape.waves, shape.slices, shape.grid};
+    record_shape([](const int* v, char* to, size_t len) {
+      snprintf(to, len, "skinny_gemm_fp8 B=%d x=%s N=%d K=%d rows/wg=%d tokens=%d waves/wg=%d k-slices=%d grid=%d", v[1],
+               v[0] ? "e4m3" : "bf16", v[2], v[3], v[4], v[5], v[6], v[7], v[8]);
+    }, v, 9);
+  }
   return s;
 }
 

@@ -28,7 +28,18 @@ struct GemmFp8Launch {
   void* Y;
   int y_bf16;
   int M, N, K;
+  int ks_n;                 // K slices (gemm_fp8_plan); their sums and one arrival counter per row group
+  float* part;
+  uint32_t* counter;
 };
+
+// Shape of the product for more than 16 tokens: row tiles a wave, K slices,
+// bytes of the slices' sums in the workspace (0: one slice).
+struct GemmFp8Plan {
+  int rt, ks;
+  size_t part_bytes;
+};
+GemmFp8Plan gemm_fp8_plan(int M, int N, int K);
 
 // The block's expert launches over 8-bit weights: ExpertLaunch with W13, W2,
 // Ws13, Ws2 in e4m3 and their scales, one row of scales for each 128 gate
@@ -40,9 +51,14 @@ struct Fp8ExpertLaunch {
   const float *s13, *s2, *ss13, *ss2;
 };
 
+// What a launch chose, for moe_last_variant.
+struct Fp8Shape {
+  int grid, waves, rows, tokens, slices;
+};
+
 hipError_t launch_quantize(const QuantizeLaunch& a, hipStream_t st);
-hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, char* desc, size_t desc_len);
-hipError_t launch_expert_up_fp8(const Fp8ExpertLaunch& a, hipStream_t st, char* desc, size_t desc_len);
-hipError_t launch_expert_down_combine_fp8(const Fp8ExpertLaunch& a, hipStream_t st, char* desc, size_t desc_len);
+hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape);
+hipError_t launch_expert_up_fp8(const Fp8ExpertLaunch& a, hipStream_t st, Fp8Shape* shape);
+hipError_t launch_expert_down_combine_fp8(const Fp8ExpertLaunch& a, hipStream_t st, Fp8Shape* shape);
 
 }  // namespace moe

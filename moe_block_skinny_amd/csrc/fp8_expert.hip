@@ -17,17 +17,26 @@ namespace moe {
 // the shared one.
 struct Fp8Entry {
   int m, I, slot0;            // tokens; expert rows; first plan slot (-1: shared, token i is token i)
+  int hbase;                  // first row of its token tiles in the tiled h
   const uint8_t *W13, *W2;
   const float *s13, *s2;
 };
 
-__device__ __forceinline__ Fp8Entry fp8_entry(const Fp8ExpertLaunch& a, const PlanView& p, int n, int idx) {
+// s_plan: the plan's words in LDS (moe_plan_words), n: its experts.
+__device__ __forceinline__ int plan_max(const Fp8ExpertLaunch& a) {
+  const int ns = a.e.B * a.e.k;
+  return ns < a.e.E ? ns : a.e.E;
+}
+
+__device__ __forceinline__ Fp8Entry fp8_entry(const Fp8ExpertLaunch& a, const int32_t* s_plan, int n, int idx) {
   Fp8Entry v;
   const size_t DB = (size_t)(a.e.d + kQBlock - 1) / kQBlock;
   if (idx < n) {
-    const size_t e = (size_t)wave_uniform(p.active[idx]);
-    v.slot0 = wave_uniform(p.offs[idx]);
-    v.m = wave_uniform(p.offs[idx + 1]) - v.slot0;
+    const int32_t* offs = s_plan + 1 + plan_max(a);
+    const size_t e = (size_t)wave_uniform(s_plan[1 + idx]);
+    v.slot0 = wave_uniform(offs[idx]);
+    v.hbase = ((a.e.B + 15) & ~15) + v.slot0 + 16 * idx;
+    v.m = wave_uniform(offs[idx + 1]) - v.slot0;
     v.I = a.e.I;
     const size_t IB = (size_t)(v.I + kQBlock - 1) / kQBlock;
     v.W13 = static_cast<const uint8_t*>(a.e.W13) + e * 2 * v.I * a.e.d;
@@ -38,6 +47,7 @@ __device__ __forceinline__ Fp8Entry fp8_entry(const Fp8ExpertLaunch& a, const Pl
     v.m = a.e.B;
     v.I = a.e.Is;
     v.slot0 = -1;
+    v.hbase = 0;
     v.W13 = static_cast<const uint8_t*>(a.e.Ws13);
     v.W2 = static_cast<const uint8_t*>(a.e.Ws2);
     v.s13 = a.ss13;
@@ -47,15 +57,29 @@ __device__ __forceinline__ Fp8Entry fp8_entry(const Fp8ExpertLaunch& a, const Pl
 }
 
 // Token and slot row of the entry's i-th token.
-__device__ __forceinline__ void fp8_token(const Fp8ExpertLaunch& a, const int32_t* slots, const Fp8Entry& v, int i,
+__device__ __forceinline__ void fp8_token(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v, int i,
                                           int& tok, int& srow) {
   if (v.slot0 >= 0) {
-    srow = slots[v.slot0 + i];
+    srow = s_plan[2 + 2 * plan_max(a) + v.slot0 + i];
     tok = srow / a.e.k;
   } else {
     tok = i;
     srow = a.e.B * a.e.k + i;
   }
+}
+
+// h as the down launch reads it: two bf16 planes (hi + lo, about 16
+// significant bits).
+//   B <= 8: slot rows [B*k + B][hld] (h_hi, h_lo); only the lanes of an
+//   entry's few tokens load.
+//   B > 8:  16-token tiles in operand order (a.e.ht_hi, ht_lo): tile row
+//   block (hbase + 16 tt) holds, for K block kb and step j, 1 KB: lane 16 g +
+//   t its 8 values -- one contiguous load per step.  From slot rows, lanes of
+//   different tokens in every quad, the same loads take a compute unit 3.5
+//   times as long (37 against 130 bytes/ns), and h crosses once per
+//   workgroup.
+__device__ __forceinline__ uint32_t h_tile(const Fp8ExpertLaunch& a, const Fp8Entry& v, int t) {
+  return (uint32_t)(v.hbase + (t & ~15)) * (uint32_t)a.e.hld;
 }
 
 // ---- gate/up + SwiGLU ----------------------------------------------------------
@@ -67,149 +91,173 @@ __device__ __forceinline__ void fp8_token(const Fp8ExpertLaunch& a, const int32_
 constexpr int kFp8Pairs = 8;
 constexpr int kKeysMaxTokens = 2;
 constexpr int kUpRouterWaves = 8;   // waves of a workgroup that scores router rows
+constexpr int kUpU = 2;             // blocks in flight a wave, B <= 8 (4: the same time, 25 more registers)
+constexpr int kUpManyWaves = 4, kUpManyWgs = 2;   // B > 8: waves a workgroup, workgroups a compute unit (256 registers)
 
-template <int XK, int NT, int U>
-__device__ __forceinline__ void up_fp8(const Fp8ExpertLaunch& a, const int32_t* slots, const Fp8Entry& v, int p0,
-                                       f32x4* s_acc) {
+template <int XK, int NT, int U, bool TILED>
+__device__ __forceinline__ void up_fp8(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v, int p0,
+                                       char* s_lds) {
+  constexpr int kWaveLds = fp8_wave_lds<XK, 1, NT>();
   constexpr int TOK = XTraits<XK>::kTokens, COLS = XTraits<XK>::kCols;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = own_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = (int)(blockDim.x >> 6);
   const int d = a.e.d, KB = (d + kQBlock - 1) / kQBlock, IB = (v.I + kQBlock - 1) / kQBlock;
-  Fp8Src<1, NT> s;
+  Fp8Src<XK, 1, NT> s;
   s.K = d;
+  s.lane = lane;
   s.x = a.e.X;
   s.xs = nullptr;
   s.w[0] = v.W13 + (size_t)p0 * d;
-  s.ra[0] = (uint32_t)(lane & 7) * (uint32_t)d;   // I is a multiple of 8: no pair is past it
-  s.rb[0] = (uint32_t)(v.I + (lane & 7)) * (uint32_t)d;
+  s.ra[0] = (uint32_t)(lane >> 3) * (uint32_t)d;   // I is a multiple of 8: no pair is past it
+  s.rb[0] = (uint32_t)(v.I + (lane >> 3)) * (uint32_t)d;
   s.sa[0] = v.s13 + (size_t)(p0 / kQBlock) * KB;
   s.sb[0] = v.s13 + (size_t)(IB + p0 / kQBlock) * KB;
   s.row_b[0] = lane >= 32;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int t = nt * TOK + x_token<XK>();
-    int tok, sr;
-    fp8_token(a, slots, v, t < v.m ? t : v.m - 1, tok, sr);
-    s.xo[nt] = (uint32_t)tok * (uint32_t)d * 2;
+#pragma unroll
+    for (int i = 0; i < x_rows<XK>(); ++i) {
+      const int t = nt * TOK + x_load_token<XK>(lane, i);
+      int tok, sr;
+      fp8_token(a, s_plan, v, t < v.m ? t : v.m - 1, tok, sr);
+      s.xo[nt][i] = (uint32_t)tok * (uint32_t)d * 2;
+    }
     s.xso[nt] = 0;
   }
   f32x4 acc[1][NT];
-  fp8_wave<XK, 1, NT, U>(s, wave, waves, acc);
+  fp8_wave<XK, 1, NT, U>(s, wave, waves, s_lds + wave * kWaveLds, acc);
+  f32x4* mine = reinterpret_cast<f32x4*>(s_lds + wave * kWaveLds);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) s_acc[(wave * NT + nt) * 64 + lane] = acc[0][nt];
+  for (int nt = 0; nt < NT; ++nt) mine[nt * 64 + lane] = acc[0][nt];
   lds_barrier();
   for (int i = threadIdx.x; i < NT * 32; i += (int)blockDim.x) {
     const int l = i & 31, nt = i >> 5, col = l & 15;
     const int t = nt * TOK + col / COLS;
     if (col % COLS || t >= v.m) continue;
-    f32x4 g = s_acc[nt * 64 + l], u = s_acc[nt * 64 + 32 + l];
+    const f32x4* sum = reinterpret_cast<const f32x4*>(s_lds) + nt * 64 + l;
+    f32x4 g = sum[0], u = sum[32];
     for (int w = 1; w < waves; ++w) {
-      g += s_acc[(w * NT + nt) * 64 + l];
-      u += s_acc[(w * NT + nt) * 64 + 32 + l];
+      g += sum[w * (kWaveLds / 16)];
+      u += sum[w * (kWaveLds / 16) + 32];
     }
     f32x4 h;
 #pragma unroll
     for (int q = 0; q < 4; ++q) h[q] = silu(g[q]) * u[q];
     int tok, sr;
-    fp8_token(a, slots, v, t, tok, sr);
+    fp8_token(a, s_plan, v, t, tok, sr);
     u32x2 hi, lo;
     uint32_t h0, l0, h1, l1;
     split_bf16x2(h[0], h[1], h0, l0);
     split_bf16x2(h[2], h[3], h1, l1);
     hi = u32x2{h0, h1};
     lo = u32x2{l0, l1};
-    const size_t o = (size_t)sr * a.e.hld + p0 + 4 * (l >> 4);
-    *reinterpret_cast<u32x2*>(h_hi(a.e) + o) = hi;
-    *reinterpret_cast<u32x2*>(h_lo(a.e) + o) = lo;
+    const int i0 = p0 + 4 * (l >> 4);
+    if constexpr (TILED) {
+      const size_t o = (size_t)h_tile(a, v, t) + (i0 >> 7) * 2048 + ((i0 >> 3) & 3) * 512 + ((i0 >> 5) & 3) * 128 + (t & 15) * 8 + (i0 & 7);
+      *reinterpret_cast<u32x2*>(a.e.ht_hi + o) = hi;
+      *reinterpret_cast<u32x2*>(a.e.ht_lo + o) = lo;
+    } else {
+      const size_t o = (size_t)sr * a.e.hld + i0;
+      *reinterpret_cast<u32x2*>(h_hi(a.e) + o) = hi;
+      *reinterpret_cast<u32x2*>(h_lo(a.e) + o) = lo;
+    }
   }
-  lds_barrier();   // s_acc is free for the next task
+  lds_barrier();   // the buffers are free for the next task
 }
 
 // MAXB: the largest batch of the instantiation (4, 8 or 64).
 template <int MAXB>
-__device__ __forceinline__ void up_fp8_dispatch(const Fp8ExpertLaunch& a, const int32_t* slots, const Fp8Entry& v,
-                                                int p0, f32x4* s_acc) {
+__device__ __forceinline__ void up_fp8_dispatch(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v,
+                                                int p0, char* s_lds) {
   if constexpr (MAXB <= 4) {
-    up_fp8<XP4, 1, 4>(a, slots, v, p0, s_acc);
+    up_fp8<XP4, 1, kUpU, false>(a, s_plan, v, p0, s_lds);
   } else if constexpr (MAXB <= 8) {
-    if (v.m <= 4) up_fp8<XP4, 1, 4>(a, slots, v, p0, s_acc);
-    else up_fp8<XP8, 1, 4>(a, slots, v, p0, s_acc);
+    if (v.m <= 4) up_fp8<XP4, 1, kUpU, false>(a, s_plan, v, p0, s_lds);
+    else up_fp8<XP8, 1, kUpU, false>(a, s_plan, v, p0, s_lds);
   } else {
     const int nt = (v.m + 15) / 16;
-    if (v.m <= 4) up_fp8<XP4, 1, 4>(a, slots, v, p0, s_acc);
-    else if (v.m <= 8) up_fp8<XP8, 1, 4>(a, slots, v, p0, s_acc);
-    else if (nt <= 1) up_fp8<XB, 1, 4>(a, slots, v, p0, s_acc);
-    else if (nt == 2) up_fp8<XB, 2, 2>(a, slots, v, p0, s_acc);
-    else if (nt == 3) up_fp8<XB, 3, 2>(a, slots, v, p0, s_acc);
-    else up_fp8<XB, 4, 2>(a, slots, v, p0, s_acc);
+    if (v.m <= 4) up_fp8<XP4, 1, 4, true>(a, s_plan, v, p0, s_lds);
+    else if (v.m <= 8) up_fp8<XP8, 1, 4, true>(a, s_plan, v, p0, s_lds);
+    else if (nt <= 1) up_fp8<XB, 1, 4, true>(a, s_plan, v, p0, s_lds);
+    else if (nt == 2) up_fp8<XB, 2, 2, true>(a, s_plan, v, p0, s_lds);
+    else if (nt == 3) up_fp8<XB, 3, 1, true>(a, s_plan, v, p0, s_lds);
+    else up_fp8<XB, 4, 1, true>(a, s_plan, v, p0, s_lds);
   }
 }
 
+// Waves of a workgroup: at most 16 of 128 registers (B <= 8), or 4 of 256.
 template <int MAXB> struct UpFp8 {
-  static constexpr int kWaves = MAXB <= 8 ? 16 : 8;   // at most; 128 or 256 registers a lane
-  static constexpr int kTiles = MAXB <= 16 ? 1 : 4;
+  static constexpr int kWaves = MAXB <= 8 ? 16 : kUpManyWaves;
+  static constexpr int kWaveLds = MAXB <= 4 ? fp8_wave_lds<XP4, 1, 1>() : MAXB <= 8 ? fp8_wave_lds<XP8, 1, 1>() : fp8_wave_lds<XB, 1, 4>();
 };
 
 template <int MAXB>
-__global__ __launch_bounds__(UpFp8<MAXB>::kWaves * 64) void expert_up_fp8_kernel(Fp8ExpertLaunch a) {
-  constexpr int NW = UpFp8<MAXB>::kWaves;
-  constexpr int kAccBytes = NW * UpFp8<MAXB>::kTiles * 64 * (int)sizeof(f32x4);
-  constexpr int kScratch = MAXB > 8 && kPlanFromIdsBytes > kAccBytes ? kPlanFromIdsBytes : kAccBytes;
+__global__ __launch_bounds__(UpFp8<MAXB>::kWaves * 64, MAXB <= 8 ? 1 : kUpManyWgs) void expert_up_fp8_kernel(Fp8ExpertLaunch a) {
   __shared__ int32_t s_plan[kMaxPlanWords];
-  __shared__ __align__(16) unsigned char s_scratch[kScratch];
-  f32x4* s_acc = reinterpret_cast<f32x4*>(s_scratch);
+  extern __shared__ __align__(16) char s_lds[];   // a buffer per wave; first plan_from_ids' scratch
   const ExpertLaunch& x = a.e;
   const int tiles_r = x.I / kFp8Pairs;
   const int tiles_s = x.Ws13 ? x.Is / kFp8Pairs : 0;
-  if constexpr (MAXB <= 8) {
+  // where the tokens are selected here: without ready words at most two of
+  // them, a wave each
+  __shared__ TopkScratch s_tk[MAXB <= 8 ? kKeysMaxTokens : 1];
+  __shared__ int32_t s_ids[64];
+  __shared__ float s_w[64];
+  __shared__ int s_order[MAXB > 8 ? kMaxB * kMaxK + kMaxB : 1];
+  if constexpr (MAXB <= 4) {
     // With the router rows in this launch, its first router_wgs workgroups
     // score them and leave
-    if (MAXB <= 4 && x.router_wgs && (int)blockIdx.x < x.router_wgs) {
+    if ((int)blockIdx.x < x.router_wgs) {
       __shared__ float s_rr[kRouterPlayedWaves * kRouterRowsInUp * 2];
       if (threadIdx.x >= kUpRouterWaves * 64) return;   // a barrier counts the waves that have not ended
       router_rows_in_up<bf16_t, kUpRouterWaves>(x, blockIdx.x, s_rr);
       return;
     }
   }
-  const int G = (int)gridDim.x - x.router_wgs;
-  int task = (int)blockIdx.x - x.router_wgs;
-  PlanView p;
-  __shared__ int s_order[MAXB > 8 ? kMaxB * kMaxK + kMaxB : 1];
-  const bool here = MAXB <= 8 && (x.logits != nullptr || x.lkeys != nullptr);
-  if (here) {
-    if constexpr (MAXB <= 8) {
-      // the shared expert's tiles need no plan: they stream while the tokens
-      // are selected
-      __shared__ TopkScratch s_tk[kKeysMaxTokens];   // here without ready words: at most 2 tokens, a wave each
-      __shared__ int32_t s_ids[64];
-      __shared__ float s_w[64];
-      if (x.ready) select_own_token(x, s_tk, s_ids, s_w);
+  if constexpr (MAXB <= 8) {
+    if (x.ready) select_own_token(x, s_tk, s_ids, s_w);
+  }
+  const int G = (int)gridDim.x - x.router_wgs, wg = (int)blockIdx.x - x.router_wgs;
+  // Tasks: the shared expert's tiles, then the routed entries'.  Where the
+  // tokens are selected here the shared tiles, which need no plan, stream
+  // meanwhile (a loop of its own: one loop over both, with the routing inside
+  // it, spilled 24 registers).  Beyond 8 tokens the entries come by falling
+  // token count, and every other round of the workgroups goes backwards, so
+  // that who had a long task first has a short one next.
+  int task = wg;
+  if constexpr (MAXB <= 8) {
+    if (x.logits || x.lkeys) {
       for (; task < tiles_s; task += G) {
-        const Fp8Entry v = fp8_entry(a, PlanView{}, 0, 0);
-        up_fp8_dispatch<MAXB>(a, nullptr, v, task * kFp8Pairs, s_acc);
+        const Fp8Entry v = fp8_entry(a, s_plan, -1, 0);
+        up_fp8_dispatch<MAXB>(a, s_plan, v, task * kFp8Pairs, s_lds);
       }
-      p = x.ready ? wait_token_plan(x, s_plan, s_tk, s_ids) : route_here<false, 1>(x, s_plan, s_tk, s_ids, s_w);
+      if (x.ready) wait_token_plan(x, s_plan, s_tk, s_ids);
+      else route_here<false, 1>(x, s_plan, s_tk, s_ids, s_w);
+    } else {
+      stage_plan(x, s_plan);
     }
   } else {
-    p = (MAXB > 8 && x.ids_in) ? plan_from_ids(x, s_plan, s_scratch) : stage_plan(x, s_plan);
-  }
-  const int n = wave_uniform(p.n);
-  if constexpr (MAXB > 8) {
-    // entries of many tokens first
-    if (threadIdx.x < 64) order_entries_by_tiles(x, p, n, s_order);
+    const PlanView p = x.ids_in ? plan_from_ids(x, s_plan, reinterpret_cast<unsigned char*>(s_lds)) : stage_plan(x, s_plan);
+    if (threadIdx.x < 64) order_entries_by_tiles(x, p, p.n, s_order);
     __syncthreads();
   }
-  const int total = tiles_s + n * tiles_r;
-  for (; task < total; task += G) {
-    const int rt = task - tiles_s;
-    int idx = n, tile = task;
-    if (rt >= 0) {
-      idx = rt / tiles_r;
-      tile = rt - idx * tiles_r;
+  const int n = wave_uniform(s_plan[0]), total = tiles_s + n * tiles_r;
+  for (int round = 0;; ++round, task += G) {
+    if constexpr (MAXB > 8) {
+      if (round * G >= total) break;
+      task = round * G + ((round & 1) ? G - 1 - wg : wg);
+      if (task >= total) continue;
+    } else {
+      if (task >= total) break;
+    }
+    int idx = n, tile = task;   // the shared expert
+    if (task >= tiles_s) {
+      idx = (task - tiles_s) / tiles_r;
+      tile = task - tiles_s - idx * tiles_r;
       if (MAXB > 8) idx = wave_uniform(s_order[idx]);
     }
-    const Fp8Entry v = fp8_entry(a, p, n, idx);
-    up_fp8_dispatch<MAXB>(a, p.slots, v, tile * kFp8Pairs, s_acc);
+    const Fp8Entry v = fp8_entry(a, s_plan, n, idx);
+    up_fp8_dispatch<MAXB>(a, s_plan, v, tile * kFp8Pairs, s_lds);
   }
 }
 
@@ -218,97 +266,141 @@ __global__ __launch_bounds__(UpFp8<MAXB>::kWaves * 64) void expert_up_fp8_kernel
 // A workgroup owns down_rows output rows (16 RT at most) of every entry; its
 // waves claim the entries in turn (many tokens first) and leave each slot's
 // outputs in an LDS tile, which is then combined in the order of combine_one.
-// h is a pair of bf16 planes (hi + lo, about 16 significant bits), so a step
-// of the product is two matrix instructions.
+// A wave requests the next entry's rows and scales before it multiplies
+// the current one.  h is a pair of bf16 planes, so a step of the
+// product is two matrix instructions.
 
 template <int RT, int KBM>
-__device__ __forceinline__ void down_fp8(const Fp8ExpertLaunch& a, const int32_t* slots, const Fp8Entry& v, int r0,
-                                         int r_end, float* s_y, int rows) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
-  const int I = v.I, IB = (I + kQBlock - 1) / kQBlock;
-  const f32x4 fzero = {0.f, 0.f, 0.f, 0.f};
-  const u32x4 zero = {0u, 0u, 0u, 0u};
+struct DownRegs {
   u32x4 wa[RT][KBM], wb[RT][KBM];
   float sc[RT][KBM];
-  // rows past the range re-read its last one (the first row of the range is uniform)
-  const uint8_t* W = v.W2 + (size_t)r0 * I;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int ra = 16 * rt + (lane & 7), rb = ra + 8, last = r_end - 1 - r0;
-    const uint32_t oa = (uint32_t)((ra < last ? ra : last) * I), ob = (uint32_t)((rb < last ? rb : last) * I);
-    const int rs = 16 * rt + 4 * g;
-#pragma unroll
-    for (int kb = 0; kb < KBM; ++kb) {
-      const int kc = kb < IB ? kb : IB - 1;
-      uint32_t c = (uint32_t)(kc * kQBlock + 16 * (lane >> 3));
-      c = c < (uint32_t)(I - 16) ? c : (uint32_t)(I - 16);
-      wa[rt][kb] = ld128_stream(W + (oa + c));
-      wb[rt][kb] = ld128_stream(W + (ob + c));
-      sc[rt][kb] = v.s2[(uint32_t)((r0 + (rs < last ? rs : last)) / kQBlock * IB + kc)];
+};
+template <int KBM>
+struct DownH {
+  u32x4 hv[KBM][4], lv[KBM][4];
+};
+
+template <int RT, int KBM, bool TILED>
+struct DownFp8 {
+  const Fp8ExpertLaunch& a;
+  const int32_t* s_plan;
+  int r0, r_end, rows;
+  float* s_y;
+  char* lds;
+  coherent_rsrc_t hi, lo;   // h planes: a lane past the entry's tokens or columns reads zeros from an offset past their end
+
+  // token tile at t0: h operands
+  __device__ __forceinline__ void load_h(const Fp8Entry& v, int t0, DownH<KBM>& h) const {
+    const int lane = threadIdx.x & 63, g = lane >> 4, t = t0 + (lane & 15);
+    uint32_t base;
+    if constexpr (TILED) {
+      base = h_tile(a, v, t0) * 2 + lane * 16;
+    } else {
+      int tok, sr;
+      fp8_token(a, s_plan, v, t < v.m ? t : v.m - 1, tok, sr);
+      base = (uint32_t)sr * (uint32_t)a.e.hld * 2 + 64 * g;
     }
-  }
-  for (int t0 = 0; t0 < v.m; t0 += 16) {
-    const int t = t0 + col;
-    int tok, sr;
-    fp8_token(a, slots, v, t < v.m ? t : v.m - 1, tok, sr);
-    const bf16_t* hh = h_hi(a.e) + (size_t)sr * a.e.hld;
-    const bf16_t* hl = h_lo(a.e) + (size_t)sr * a.e.hld;
-    u32x4 hv[KBM][4], lv[KBM][4];
 #pragma unroll
     for (int kb = 0; kb < KBM; ++kb)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = kb * kQBlock + 32 * g + 8 * j;
-        const int cc = c < I - 8 ? c : I - 8;
-        hv[kb][j] = ld128(hh + cc);
-        lv[kb][j] = ld128(hl + cc);
-        if (c >= I) hv[kb][j] = lv[kb][j] = zero;
+        const bool ok = t < v.m && kb * kQBlock + 32 * g + 8 * j < v.I;
+        const uint32_t o = ok ? base + (TILED ? kb * 4096 + j * 1024 : kb * 256 + 16 * j) : 0xfffffff0u;
+        h.hv[kb][j] = __builtin_amdgcn_raw_buffer_load_b128(hi, o, 0, 0);
+        h.lv[kb][j] = __builtin_amdgcn_raw_buffer_load_b128(lo, o, 0, 0);
       }
+  }
+
+  __device__ __forceinline__ void load(const Fp8Entry& v, DownRegs<RT, KBM>& r) const {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const int I = v.I, IB = (I + kQBlock - 1) / kQBlock;
+    // rows past the range re-read its last one
+    const uint8_t* W = v.W2 + (size_t)r0 * I;
+    const int last = r_end - 1 - r0;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      f32x4 y = fzero;
+      const int ra = 16 * rt + (lane >> 3), rb = ra + 8, rs = 16 * rt + 4 * g;
+      const uint32_t oa = (uint32_t)((ra < last ? ra : last) * I), ob = (uint32_t)((rb < last ? rb : last) * I);
 #pragma unroll
       for (int kb = 0; kb < KBM; ++kb) {
-        if (kb < IB) {
-          u32x4 lo, hi;
-          w_operand(wa[rt][kb], wb[rt][kb], lo, hi);
-          const int c0 = kb * kQBlock + 32 * g;
-          if (c0 >= I) lo = zero;
-          if (c0 + 16 >= I) hi = zero;
-          bf16x8 wv[4];
-          wv[0] = widen8(lo[0], lo[1]);
-          wv[1] = widen8(lo[2], lo[3]);
-          wv[2] = widen8(hi[0], hi[1]);
-          wv[3] = widen8(hi[2], hi[3]);
-          f32x4 q = fzero;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], __builtin_bit_cast(bf16x8, hv[kb][j]), q, 0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], __builtin_bit_cast(bf16x8, lv[kb][j]), q, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(sc[rt][kb], q[i], y[i]);
-        }
+        const int kc = kb < IB ? kb : IB - 1;
+        uint32_t c = (uint32_t)(kc * kQBlock + 16 * (lane & 7));
+        c = c < (uint32_t)(I - 16) ? c : (uint32_t)(I - 16);
+        r.wa[rt][kb] = ld128_stream(W + (oa + c));
+        r.wb[rt][kb] = ld128_stream(W + (ob + c));
+        r.sc[rt][kb] = v.s2[(uint32_t)((r0 + (rs < last ? rs : last)) / kQBlock * IB + kc)];
       }
-      const int r = 16 * rt + 4 * g;
-      if (t < v.m && r < rows) *reinterpret_cast<f32x4*>(s_y + (size_t)sr * rows + r) = y;
     }
   }
-}
 
-constexpr int kFp8DownWaves = 8;
+  // the entry's rows from registers to the wave's buffer
+  __device__ __forceinline__ void keep(const DownRegs<RT, KBM>& r, float (&sc)[RT][KBM]) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int kb = 0; kb < KBM; ++kb) {
+        rows128_store(lane, lds + (rt * KBM + kb) * 2048, r.wa[rt][kb], r.wb[rt][kb]);
+        sc[rt][kb] = r.sc[rt][kb];
+      }
+  }
 
-template <int RT, int KBM>
-__global__ __launch_bounds__(kFp8DownWaves * 64) void expert_down_combine_fp8_kernel(Fp8ExpertLaunch a) {
+  __device__ __forceinline__ void products(const Fp8Entry& v, const float (&sc)[RT][KBM], DownH<KBM>& h) const {
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int I = v.I, IB = (I + kQBlock - 1) / kQBlock;
+    const f32x4 fzero = {0.f, 0.f, 0.f, 0.f};
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    for (int t0 = 0;;) {
+      const int t = t0 + col;
+      int tok, sr;
+      fp8_token(a, s_plan, v, t < v.m ? t : v.m - 1, tok, sr);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        f32x4 y = fzero;
+#pragma unroll
+        for (int kb = 0; kb < KBM; ++kb) {
+          if (kb < IB) {
+            u32x4 w0, w1;
+            rows128_load(lane, lds + (rt * KBM + kb) * 2048, w0, w1);
+            const int c0 = kb * kQBlock + 32 * g;
+            if (c0 >= I) w0 = zero;
+            if (c0 + 16 >= I) w1 = zero;
+            const bf16x8 wv[4] = {widen8(w0[0], w0[1]), widen8(w0[2], w0[3]), widen8(w1[0], w1[1]), widen8(w1[2], w1[3])};
+            f32x4 q = fzero;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], __builtin_bit_cast(bf16x8, h.hv[kb][j]), q, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], __builtin_bit_cast(bf16x8, h.lv[kb][j]), q, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(sc[rt][kb], q[i], y[i]);
+          }
+        }
+        const int rr = 16 * rt + 4 * g;
+        if (t < v.m && rr < rows) *reinterpret_cast<f32x4*>(s_y + (size_t)sr * rows + rr) = y;
+        __builtin_amdgcn_sched_barrier(0);   // one tile's operands at a time (registers)
+      }
+      t0 += 16;
+      if (t0 >= v.m) break;
+      load_h(v, t0, h);
+    }
+  }
+};
+
+template <int KBM> struct DownWaves { static constexpr int kMax = KBM == 1 ? 16 : 12; };
+
+template <int RT, int KBM, bool TILED>
+__global__ __launch_bounds__(DownWaves<KBM>::kMax * 64) void expert_down_combine_fp8_kernel(Fp8ExpertLaunch a) {
   __shared__ int32_t s_plan[kMaxPlanWords];
   __shared__ float s_tw[kMaxB * kMaxK];
   __shared__ int s_order[kMaxB * kMaxK + kMaxB];
   __shared__ int s_next;
-  extern __shared__ f32x4 s_out[];
-  float* s_y = reinterpret_cast<float*>(s_out);   // [B*k + B][rows], rows a multiple of 4
+  extern __shared__ __align__(16) char s_dyn[];   // a buffer per wave, then s_y [B*k + B][rows], rows a multiple of 4
   const ExpertLaunch& x = a.e;
   const int rows = x.down_rows;
+  const int nw = (int)(blockDim.x >> 6), wave = wave_uniform(threadIdx.x >> 6);
+  float* s_y = reinterpret_cast<float*>(s_dyn + nw * (RT * KBM * 2048));
   // the router rows' keys of the gate/up launch, zero again for the next call
   if (x.lkeys) {
     const int n = x.B * x.E;
@@ -318,20 +410,46 @@ __global__ __launch_bounds__(kFp8DownWaves * 64) void expert_down_combine_fp8_ke
   for (int i = threadIdx.x; i < x.B * x.k; i += blockDim.x) s_tw[i] = x.topk_w[i];
   const PlanView p = stage_plan(x, s_plan);
   const int n = wave_uniform(p.n), ne = n + (x.Ws13 ? 1 : 0);
-  const int nw = (int)(blockDim.x >> 6), wave = wave_uniform(threadIdx.x >> 6);
   if (wave == 0) {
     order_entries_by_tiles(x, p, ne, s_order);
     if ((threadIdx.x & 63) == 0) s_next = nw;
   }
   __syncthreads();
   const int r0 = (int)blockIdx.x * rows;
-  const int r_end = r0 + rows < x.d ? r0 + rows : x.d;
-  for (int u = wave; u < ne;) {
-    const Fp8Entry v = fp8_entry(a, p, n, wave_uniform(s_order[u]));
-    down_fp8<RT, KBM>(a, p.slots, v, r0, r_end, s_y, rows);
-    int nx = 0;
-    if ((threadIdx.x & 63) == 0) nx = atomicAdd(&s_next, 1);
-    u = wave_uniform(nx);
+  const int plane = (TILED ? ht_rows(x.B, x.k, x.E) : x.B * x.k + x.B) * x.hld * 2;
+  const void* hh = TILED ? x.ht_hi : h_hi(x);
+  const void* hl = TILED ? x.ht_lo : h_lo(x);
+  const DownFp8<RT, KBM, TILED> d = {a, s_plan, r0, r0 + rows < x.d ? r0 + rows : x.d, rows, s_y,
+                                     s_dyn + wave * (RT * KBM * 2048),
+                                     __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(hh), 0, plane, 0x00020000),
+                                     __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(hl), 0, plane, 0x00020000)};
+  auto claim = [&] {
+    int u = 0;
+    if ((threadIdx.x & 63) == 0) u = atomicAdd(&s_next, 1);
+    return wave_uniform(u);
+  };
+  auto entry = [&](int u) { return fp8_entry(a, s_plan, n, wave_uniform(s_order[u])); };
+  if (wave < ne) {
+    // The current entry's rows go to the wave's buffer as they arrive, which
+    // frees their registers for the next entry's; its h is requested before
+    // those, since loads return in order.
+    DownRegs<RT, KBM> r;
+    DownH<KBM> h;
+    float sc[RT][KBM];
+    Fp8Entry v = entry(wave);
+    d.load(v, r);
+    for (;;) {
+      d.load_h(v, 0, h);
+      d.keep(r, sc);
+      const int u = claim();
+      if (u >= ne) break;
+      const Fp8Entry next = entry(u);
+      d.load(next, r);
+      __builtin_amdgcn_sched_barrier(0);
+      d.products(v, sc, h);
+      v = next;
+    }
+    d.products(v, sc, h);
   }
   __syncthreads();
   const int has_shared = x.Ws13 ? 1 : 0;
@@ -360,50 +478,70 @@ static int split_waves(int KB, int U, int maxw) {
   return (KB + U * steps - 1) / (U * steps);
 }
 
-hipError_t launch_expert_up_fp8(const Fp8ExpertLaunch& a0, hipStream_t st, char* desc, size_t len) {
+hipError_t launch_expert_up_fp8(const Fp8ExpertLaunch& a0, hipStream_t st, Fp8Shape* shape) {
   Fp8ExpertLaunch a = a0;
   const ExpertLaunch& x = a.e;
   const int KB = (x.d + kQBlock - 1) / kQBlock;
   const int ns = x.B * x.k;
   int g = (ns < x.E ? ns : x.E) * (x.I / kFp8Pairs) + (x.Ws13 ? x.Is / kFp8Pairs : 0);
-  int w = split_waves(KB, 4, x.B <= 8 ? 16 : 8);
-  // the router rows and the selections need their waves
-  if (w < kUpRouterWaves) w = kUpRouterWaves;
-  // the whole grid resident at once: no workgroup waits for one that has not started
-  const int cap = kCUs * (x.B <= 8 ? 1 : 1);
+  // B <= 8: as many waves to a workgroup as leave every task resident at once
+  // (16 waves a compute unit): a task's bytes are then all in flight where
+  // there are few tasks, and small workgroups finish evenly where there are
+  // many.  Router rows and selections need four.
+  int w, cap;
+  if (x.B <= 8) {
+    w = split_waves(KB, kUpU, g <= kCUs ? 16 : 8);
+    if (w < kUpRouterWaves) w = kUpRouterWaves;
+    cap = kCUs * (16 / w);
+  } else {
+    w = split_waves(KB, 4, kUpManyWaves);
+    cap = kCUs * kUpManyWgs;
+  }
   if (g > cap) g = cap;
   if (x.ready && g < x.B) g = x.B;
   const dim3 grid((unsigned)(g + x.router_wgs)), block((unsigned)(64 * w));
-  if (x.B <= 4) launch(K_EXPERT_UP, expert_up_fp8_kernel<4>, grid, block, 0, st, a);
-  else if (x.B <= 8) launch(K_EXPERT_UP, expert_up_fp8_kernel<8>, grid, block, 0, st, a);
-  else launch(K_EXPERT_UP, expert_up_fp8_kernel<64>, grid, block, 0, st, a);
-  if (desc)
-    snprintf(desc, len, "fp8 up grid=%d waves/wg=%d%s%s", g, w, x.router_wgs ? " +router rows" : "",
-             (x.logits || x.lkeys) ? " +top-k/plan" : "");
+  auto lds = [&](int wave, int least) { return (uint32_t)(w * wave > least ? w * wave : least); };
+  if (x.B <= 4) launch(K_EXPERT_UP, expert_up_fp8_kernel<4>, grid, block, lds(UpFp8<4>::kWaveLds, 0), st, a);
+  else if (x.B <= 8) launch(K_EXPERT_UP, expert_up_fp8_kernel<8>, grid, block, lds(UpFp8<8>::kWaveLds, 0), st, a);
+  else launch(K_EXPERT_UP, expert_up_fp8_kernel<64>, grid, block, lds(UpFp8<64>::kWaveLds, kPlanFromIdsBytes), st, a);
+  *shape = {g, w, 0, 0, 0};
   return hipGetLastError();
 }
 
-hipError_t launch_expert_down_combine_fp8(const Fp8ExpertLaunch& a0, hipStream_t st, char* desc, size_t len) {
+template <int RT, int KBM>
+static void go_down(const Fp8ExpertLaunch& a, int nw, int y_bytes, dim3 grid, hipStream_t st) {
+  const dim3 block((unsigned)(64 * nw));
+  const uint32_t lds = (uint32_t)(y_bytes + nw * RT * KBM * 2048);
+  if (a.e.ht_hi) launch(K_EXPERT_DOWN, (expert_down_combine_fp8_kernel<RT, KBM, true>), grid, block, lds, st, a);
+  else launch(K_EXPERT_DOWN, (expert_down_combine_fp8_kernel<RT, KBM, false>), grid, block, lds, st, a);
+}
+
+hipError_t launch_expert_down_combine_fp8(const Fp8ExpertLaunch& a0, hipStream_t st, Fp8Shape* shape) {
   Fp8ExpertLaunch a = a0;
   ExpertLaunch& x = a.e;
-  // rows split evenly over the compute units in multiples of 4, 16 to 32 a workgroup
+  const int longest = x.Ws13 && x.Is > x.I ? x.Is : x.I, kbm = longest <= kQBlock ? 1 : 2;
+  int nw = max_entries(x);
+  const int maxw = kbm == 1 ? DownWaves<1>::kMax : DownWaves<2>::kMax;
+  if (nw > maxw) nw = maxw;
+  // rows split evenly over the compute units in multiples of 4, 16 to 32 a
+  // workgroup, and as many as fit in LDS beside the waves' buffers (160 KB,
+  // of which the plan takes 17 KB)
+  const int slots = x.B * x.k + x.B;
   int rows = 4 * ((x.d + 4 * kCUs - 1) / (4 * kCUs));
   rows = rows < 16 ? 16 : (rows > 32 ? 32 : rows);
+  auto fits = [&](int r) { return slots * r * 4 + nw * (r > 16 ? 2 : 1) * kbm * 2048 <= 143 * 1024; };
+  while (nw > 8 && !fits(rows)) --nw;
+  while (rows > 4 && !fits(rows)) rows -= 4;
   x.down_rows = rows;
-  const int g = (x.d + rows - 1) / rows;
-  int nw = max_entries(x);
-  if (nw > kFp8DownWaves) nw = kFp8DownWaves;
-  const size_t lds = (size_t)(x.B * x.k + x.B) * rows * sizeof(float);
-  const dim3 grid((unsigned)g), block((unsigned)(64 * nw));
-  const int longest = x.Ws13 && x.Is > x.I ? x.Is : x.I;
+  const int g = (x.d + rows - 1) / rows, y = slots * rows * 4;
   if (rows <= 16) {
-    if (longest <= kQBlock) launch(K_EXPERT_DOWN, (expert_down_combine_fp8_kernel<1, 1>), grid, block, lds, st, a);
-    else launch(K_EXPERT_DOWN, (expert_down_combine_fp8_kernel<1, 2>), grid, block, lds, st, a);
+    if (kbm == 1) go_down<1, 1>(a, nw, y, dim3((unsigned)g), st);
+    else go_down<1, 2>(a, nw, y, dim3((unsigned)g), st);
   } else {
-    if (longest <= kQBlock) launch(K_EXPERT_DOWN, (expert_down_combine_fp8_kernel<2, 1>), grid, block, lds, st, a);
-    else launch(K_EXPERT_DOWN, (expert_down_combine_fp8_kernel<2, 2>), grid, block, lds, st, a);
+    if (kbm == 1) go_down<2, 1>(a, nw, y, dim3((unsigned)g), st);
+    else go_down<2, 2>(a, nw, y, dim3((unsigned)g), st);
   }
-  if (desc) snprintf(desc, len, "fp8 down+combine grid=%d rows/wg=%d waves/wg=%d", g, rows, nw);
+  *shape = {g, nw, rows, 0, 0};
   return hipGetLastError();
 }
 

@@ -1,6 +1,8 @@
 // fp8_gemm.hip -- the 8-bit quantiser and the dense skinny product over 8-bit
 // weights (fp8_core.hpp).
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "fp8.hpp"
 #include "fp8_core.hpp"
@@ -173,16 +175,45 @@ hipError_t launch_quantize(const QuantizeLaunch& a0, hipStream_t st) {
 // A workgroup owns 16 RT rows of W over all of K; its waves split K by blocks
 // and meet once, in LDS, in wave order (deterministic).
 
+// Results of tokens t, rows n .. n + 3 (only those below N are there).
+__device__ __forceinline__ void store_rows(const GemmFp8Launch& a, int t, int n, f32x4 v) {
+  const size_t o = (size_t)t * a.N + n;
+  if ((a.N & 3) == 0) {
+    if (a.R) {
+      const u32x2 r = *reinterpret_cast<const u32x2*>(a.R + o);
+      v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
+    }
+    if (a.y_bf16) {
+      const u32x2 p = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                       (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+      *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(a.Y) + o) = p;
+    } else {
+      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.Y) + o) = v;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (n + q >= a.N) break;
+      const float y = a.R ? v[q] + bf16_to_f32(a.R[o + q]) : v[q];
+      if (a.y_bf16) reinterpret_cast<bf16_t*>(a.Y)[o + q] = f32_to_bf16(y);
+      else reinterpret_cast<float*>(a.Y)[o + q] = y;
+    }
+  }
+}
+
 template <int XK, int RT, int NT, int U, int MAXW>
 __global__ __launch_bounds__(MAXW * 64) void gemm_fp8_kernel(GemmFp8Launch a) {
-  extern __shared__ f32x4 s_acc[];   // [waves][RT][NT][64]
+  // a wave's buffer, then its sums [RT][NT][64]
+  extern __shared__ __align__(16) char s_lds[];
+  constexpr int kWaveLds = fp8_wave_lds<XK, RT, NT>();
   constexpr int TOK = XTraits<XK>::kTokens, COLS = XTraits<XK>::kCols;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = (int)(blockDim.x >> 6);
   const int KB = (a.K + kQBlock - 1) / kQBlock;
   const int r0 = (int)blockIdx.x * 16 * RT;
-  Fp8Src<RT, NT> s;
+  Fp8Src<XK, RT, NT> s;
   s.K = a.K;
+  s.lane = lane;
   s.x = a.X;
   s.xs = a.Xs;
   const int xb = x_e4m3(XK) ? 1 : 2;
@@ -190,7 +221,7 @@ __global__ __launch_bounds__(MAXW * 64) void gemm_fp8_kernel(GemmFp8Launch a) {
   for (int rt = 0; rt < RT; ++rt) {
     // rows past N re-read the last one and are not stored
     const int base = r0 + 16 * rt < a.N ? r0 + 16 * rt : a.N - 1;
-    const int ra = base + (lane & 7), rb = ra + 8;
+    const int ra = base + (lane >> 3), rb = ra + 8;
     s.w[rt] = a.W + (size_t)base * a.K;
     s.ra[rt] = (uint32_t)((ra < a.N ? ra : a.N - 1) - base) * (uint32_t)a.K;
     s.rb[rt] = (uint32_t)((rb < a.N ? rb : a.N - 1) - base) * (uint32_t)a.K;
@@ -199,78 +230,239 @@ __global__ __launch_bounds__(MAXW * 64) void gemm_fp8_kernel(GemmFp8Launch a) {
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    int t = nt * TOK + x_token<XK>();
-    t = t < a.M ? t : a.M - 1;
-    s.xo[nt] = (uint32_t)t * (uint32_t)a.K * xb;
-    s.xso[nt] = (uint32_t)t * (uint32_t)KB;
+    auto token = [&](int t) { return (uint32_t)(nt * TOK + t < a.M ? nt * TOK + t : a.M - 1); };
+#pragma unroll
+    for (int i = 0; i < x_rows<XK>(); ++i) s.xo[nt][i] = token(x_load_token<XK>(lane, i)) * (uint32_t)a.K * xb;
+    s.xso[nt] = token(x_column_token<XK>(lane)) * (uint32_t)KB;
   }
   f32x4 acc[RT][NT];
-  fp8_wave<XK, RT, NT, U>(s, wave, waves, acc);
+  fp8_wave<XK, RT, NT, U>(s, wave, waves, s_lds + wave * kWaveLds, acc);
+  f32x4* mine = reinterpret_cast<f32x4*>(s_lds + wave * kWaveLds);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s_acc[((wave * RT + rt) * NT + nt) * 64 + lane] = acc[rt][nt];
+    for (int nt = 0; nt < NT; ++nt) mine[(rt * NT + nt) * 64 + lane] = acc[rt][nt];
   __syncthreads();
   for (int i = threadIdx.x; i < RT * NT * 64; i += (int)blockDim.x) {
     const int l = i & 63, nt = (i >> 6) % NT, rt = (i >> 6) / NT;
     const int col = l & 15;
     const int t = nt * TOK + col / COLS, n = r0 + 16 * rt + 4 * (l >> 4);
     if (col % COLS || t >= a.M || n >= a.N) continue;
-    f32x4 v = s_acc[i];
-    for (int w = 1; w < waves; ++w) v += s_acc[w * RT * NT * 64 + i];
-    const size_t o = (size_t)t * a.N + n;
-    if ((a.N & 3) == 0) {
-      if (a.R) {
-        const u32x2 r = *reinterpret_cast<const u32x2*>(a.R + o);
-        v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
-      }
-      if (a.y_bf16) {
-        const u32x2 p = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                         (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
-        *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(a.Y) + o) = p;
-      } else {
-        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.Y) + o) = v;
-      }
-    } else {
+    const f32x4* sum = reinterpret_cast<const f32x4*>(s_lds) + i;
+    f32x4 v = sum[0];
+    for (int w = 1; w < waves; ++w) v += sum[w * (kWaveLds / 16)];
+    store_rows(a, t, n, v);
+  }
+}
+
+// More than 16 tokens: 64 RT rows of W and one of a.ks_n slices of K for each
+// workgroup (shared_product).  The slices' sums meet in the workspace: the
+// last workgroup of a row group to arrive adds them in slice order.
+template <int RT, int NT, bool E8, int U>
+__global__ __launch_bounds__(kSharedWaves * 64) void gemm_fp8_shared_kernel(GemmFp8Launch a) {
+  extern __shared__ __align__(16) char s_lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 2, rg = wave & 3;
+  const int KB = (a.K + kQBlock - 1) / kQBlock;
+  const int tile = (int)blockIdx.x / a.ks_n, ks = (int)blockIdx.x % a.ks_n;
+  const int r0 = (tile * 4 + rg) * 16 * RT;
+  SharedSrc<RT, NT, E8> s;
+  s.K = a.K;
+  s.x = a.X;
+  s.xs = a.Xs;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (n + q >= a.N) break;
-        const float y = a.R ? v[q] + bf16_to_f32(a.R[o + q]) : v[q];
-        if (a.y_bf16) reinterpret_cast<bf16_t*>(a.Y)[o + q] = f32_to_bf16(y);
-        else reinterpret_cast<float*>(a.Y)[o + q] = y;
+  for (int rt = 0; rt < RT; ++rt) {
+    // rows past N re-read the last one and are not stored
+    const int base = r0 + 16 * rt < a.N ? r0 + 16 * rt : a.N - 1;
+    const int ra = base + (lane >> 3), rb = ra + 8;
+    s.w[rt] = a.W + (size_t)base * a.K;
+    s.ra[rt] = (uint32_t)((ra < a.N ? ra : a.N - 1) - base) * (uint32_t)a.K;
+    s.rb[rt] = (uint32_t)((rb < a.N ? rb : a.N - 1) - base) * (uint32_t)a.K;
+    s.sa[rt] = s.sb[rt] = a.Ws + (size_t)(base / kQBlock) * KB;
+    s.row_b[rt] = false;
+  }
+  auto token = [&](int t) { return (uint32_t)(t < a.M ? t : a.M - 1); };
+#pragma unroll
+  for (int i = 0; i < SharedSrc<RT, NT, E8>::XL; ++i)
+    s.xo[i] = token(shared_load_token<E8>(i)) * (uint32_t)a.K * (E8 ? 1 : 2);
+  s.xso = token(16 * rg + (lane & 15)) * (uint32_t)KB;
+  // this slice's blocks, then the half's
+  const int b0 = (int)((int64_t)KB * ks / a.ks_n), b1 = (int)((int64_t)KB * (ks + 1) / a.ks_n);
+  const int iters = (b1 - b0 + 1) / 2;
+  const int kb0 = b0 + half * iters, n = half ? b1 - b0 - iters : iters;
+  f32x4 acc[RT][NT];
+  shared_product<RT, NT, E8, U>(s, kb0, n, iters, s_lds, acc);
+  // the second half's sums to the first; pieces of 16 rows x 16 tokens,
+  // piece i = (row group * RT + rt) * NT + nt
+  constexpr int kPieces = 4 * RT * NT;
+  f32x4* sums = reinterpret_cast<f32x4*>(s_lds);   // [kPieces][64]
+  f32x4* mine = sums + rg * RT * NT * 64 + lane;
+  if (half == 1) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mine[(rt * NT + nt) * 64] = acc[rt][nt];
+  }
+  __syncthreads();
+  if (half == 0) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        acc[rt][nt] += mine[(rt * NT + nt) * 64];
+        mine[(rt * NT + nt) * 64] = acc[rt][nt];
       }
+  }
+  if (a.ks_n > 1) {
+    const coherent_rsrc_t prs = coherent_rsrc(a.part);
+    auto off = [&](int slice, int i) { return (uint32_t)((((tile * a.ks_n + slice) * kPieces + i) * 64 + lane) * 16); };
+    if (half == 0) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          st_coherent4(prs, off(ks, (rg * RT + rt) * NT + nt), __builtin_bit_cast(u32x4, acc[rt][nt]));
     }
+    __shared__ int s_last;
+    if (!arrive_last(a.counter + tile, (uint32_t)a.ks_n, &s_last)) return;
+    // the eight waves share the pieces; kSlices slices are requested at a time
+    constexpr int kPer = (kPieces + kSharedWaves - 1) / kSharedWaves, kSlices = 4;
+    f32x4 v[kPer];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int q0 = 0; q0 < a.ks_n; q0 += kSlices) {
+      u32x4 pv[kSlices][kPer];
+#pragma unroll
+      for (int q = 0; q < kSlices; ++q)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          const int i = wave + kSharedWaves * p;
+          pv[q][p] = ld_coherent4(prs, off(q0 + q < a.ks_n ? q0 + q : q0, i < kPieces ? i : 0));
+        }
+#pragma unroll
+      for (int q = 0; q < kSlices; ++q)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p)
+          if (q0 + q < a.ks_n) v[p] += __builtin_bit_cast(f32x4, pv[q][p]);
+    }
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const int i = wave + kSharedWaves * p;
+      if (i < kPieces) sums[i * 64 + lane] = v[p];
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = wave; i < kPieces; i += kSharedWaves) {
+    const int t = 16 * (i % NT) + (lane & 15), row = (tile * 4 * RT + i / NT) * 16 + 4 * (lane >> 4);
+    if (t < a.M && row < a.N) store_rows(a, t, row, sums[i * 64 + lane]);
   }
 }
 
 template <int XK, int RT, int NT, int U, int MAXW>
-static void go(const GemmFp8Launch& a, hipStream_t st, char* desc, size_t len) {
+static void go(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
   const int KB = (a.K + kQBlock - 1) / kQBlock;
-  int w = (KB + U - 1) / U;
-  if (w > MAXW) w = MAXW;
+  const int steps = (KB + U * MAXW - 1) / (U * MAXW);
+  const int w = (KB + U * steps - 1) / (U * steps);
   const int g = (a.N + 16 * RT - 1) / (16 * RT);
   launch(K_SKINNY, (gemm_fp8_kernel<XK, RT, NT, U, MAXW>), dim3((unsigned)g), dim3((unsigned)(64 * w)),
-         (uint32_t)(w * RT * NT * 64 * sizeof(f32x4)), st, a);
-  if (desc)
-    snprintf(desc, len, "fp8 x=%s M=%d N=%d K=%d rows/wg=%d tokens/tile=%d waves/wg=%d grid=%d", x_e4m3(XK) ? "e4m3" : "bf16",
-             a.M, a.N, a.K, 16 * RT, NT * XTraits<XK>::kTokens, w, g);
+         (uint32_t)(w * fp8_wave_lds<XK, RT, NT>()), st, a);
+  *shape = {g, w, 16 * RT, NT * XTraits<XK>::kTokens, 1};
 }
 
-hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, char* desc, size_t len) {
+// Which kernel takes a product of more than 16 tokens, measured at B = 64 or
+// 32 (us, shared against split waves): 7168 x 7168 bf16 22.0 / 24.4, e4m3
+// 23.7 / 23.0; 1536 x 7168 10.5 / 12.3 (bf16, 32), 14.0 / 17.4 (e4m3, 64);
+// 7168 x 2048 (e4m3, 32) 10.6 / 6.5; 1001 x 1040 8.5 / 5.3.  A short K leaves
+// the shared kernel too few blocks to hide its start and its meeting.
+constexpr int kSharedMinTokens = 17, kSharedMinK = 4096;
+
+// K slices and row tiles of the shared kernel: 64 RT rows a workgroup, and as
+// many slices as put a workgroup on every compute unit, of at least four
+// blocks (two a half), while the last workgroup of a row group reads at most
+// kMaxPartialBytes (one or two round trips).  RT = 2 from N = 6400 on: at
+// N = 7168 22.0 us against 26.2 with RT = 1, at 1536 no difference.
+GemmFp8Plan gemm_fp8_plan(int M, int N, int K) {
+  constexpr int kCUs = 256, kMaxPartialBytes = 128 * 1024, kMinNForTwo = 6400;
+  GemmFp8Plan p = {0, 1, 0};
+  if (M < kSharedMinTokens || K < kSharedMinK) return p;
+  const int KB = (K + kQBlock - 1) / kQBlock, nt = (M + 15) / 16;
+  p.rt = N >= kMinNForTwo ? 2 : 1;
+  const int rg = (N + 64 * p.rt - 1) / (64 * p.rt);
+  int ks = kCUs / rg;
+  const int most = kMaxPartialBytes / (64 * p.rt * 16 * nt * 4);
+  if (ks > most) ks = most;
+  if (ks > KB / 4) ks = KB / 4;
+  if (ks < 1) ks = 1;
+  p.ks = ks;
+  p.part_bytes = ks > 1 ? (size_t)rg * ks * 64 * p.rt * 16 * nt * 4 : 0;
+  return p;
+}
+
+template <int RT, int NT, bool E8, int U>
+static void go_shared(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
+  const int g = (a.N + 64 * RT - 1) / (64 * RT) * a.ks_n;
+  launch(K_SKINNY, (gemm_fp8_shared_kernel<RT, NT, E8, U>), dim3((unsigned)g), dim3(kSharedWaves * 64),
+         (uint32_t)shared_lds<RT, NT>(), st, a);
+  *shape = {g, kSharedWaves, 64 * RT, 16 * NT, a.ks_n};
+}
+
+// Two row tiles a wave (half the activation bytes for a weight byte) once the
+// rows still make a workgroup for every other compute unit.
+constexpr int kMinNForTwoTiles = 4096;
+
+hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
+  const GemmFp8Plan p = gemm_fp8_plan(a.M, a.N, a.K);
   const int nt = (a.M + 15) / 16;
+  if (p.rt) {
+    GemmFp8Launch b = a;
+    b.ks_n = p.ks;
+    auto pick = [&](auto E) {
+      constexpr bool E8 = decltype(E)::value;
+      constexpr int U = 2;   // 7168 x 7168, B = 64: 22.0 us, 24.4 at 3, 25.1 at 4 (registers)
+      if (p.rt == 1) {
+        if (nt == 2) go_shared<1, 2, E8, U>(b, st, shape);
+        else if (nt == 3) go_shared<1, 3, E8, U>(b, st, shape);
+        else go_shared<1, 4, E8, U>(b, st, shape);
+      } else {
+        if (nt == 2) go_shared<2, 2, E8, U>(b, st, shape);
+        else if (nt == 3) go_shared<2, 3, E8, U>(b, st, shape);
+        else go_shared<2, 4, E8, U>(b, st, shape);
+      }
+    };
+    if (a.x_e4m3) pick(std::true_type());
+    else pick(std::false_type());
+    return hipGetLastError();
+  }
+  // Waves and blocks in flight: up to 8 tokens 8 waves of 2 blocks (two or
+  // more workgroups a compute unit; 7168 x 7168, B = 1: 10.8 us against 12.9
+  // with 14 waves of 4), up to 16 tokens 4 waves of 2 (16.1 against 18.9 with
+  // 8 of 4), beyond that 4 waves.
   if (a.x_e4m3) {
-    if (a.M <= 8) go<X8P, 1, 1, 4, 16>(a, st, desc, len);
-    else if (nt <= 1) go<X8, 1, 1, 4, 16>(a, st, desc, len);
-    else if (nt == 2) go<X8, 2, 2, 2, 8>(a, st, desc, len);
-    else if (nt == 3) go<X8, 2, 3, 2, 8>(a, st, desc, len);
-    else go<X8, 2, 4, 2, 8>(a, st, desc, len);
+    if (a.M <= 8) go<X8P, 1, 1, 2, 8>(a, st, shape);
+    else if (nt <= 1) go<X8, 1, 1, 2, 4>(a, st, shape);
+    else if (a.N < kMinNForTwoTiles) {
+      if (nt == 2) go<X8, 1, 2, 2, 8>(a, st, shape);
+      else if (nt == 3) go<X8, 1, 3, 2, 8>(a, st, shape);
+      else go<X8, 1, 4, 2, 8>(a, st, shape);
+    } else {
+      if (nt == 2) go<X8, 2, 2, 2, 4>(a, st, shape);
+      else if (nt == 3) go<X8, 2, 3, 2, 4>(a, st, shape);
+      else go<X8, 2, 4, 2, 4>(a, st, shape);
+    }
   } else {
-    if (a.M <= 4) go<XP4, 1, 1, 4, 16>(a, st, desc, len);
-    else if (a.M <= 8) go<XP8, 1, 1, 4, 16>(a, st, desc, len);
-    else if (nt <= 1) go<XB, 1, 1, 4, 16>(a, st, desc, len);
-    else if (nt == 2) go<XB, 2, 2, 2, 8>(a, st, desc, len);
-    else if (nt == 3) go<XB, 2, 3, 2, 8>(a, st, desc, len);
-    else go<XB, 2, 4, 2, 8>(a, st, desc, len);
+    if (a.M <= 4) go<XP4, 1, 1, 2, 8>(a, st, shape);
+    else if (a.M <= 8) go<XP8, 1, 1, 2, 8>(a, st, shape);
+    else if (nt <= 1) go<XB, 1, 1, 2, 4>(a, st, shape);
+    else if (a.N < kMinNForTwoTiles) {
+      if (nt == 2) go<XB, 1, 2, 2, 8>(a, st, shape);
+      else if (nt == 3) go<XB, 1, 3, 2, 8>(a, st, shape);
+      else go<XB, 1, 4, 1, 8>(a, st, shape);
+    } else {
+      if (nt == 2) go<XB, 2, 2, 2, 4>(a, st, shape);
+      else if (nt == 3) go<XB, 2, 3, 1, 4>(a, st, shape);
+      else go<XB, 2, 4, 1, 4>(a, st, shape);
+    }
   }
   return hipGetLastError();
 }

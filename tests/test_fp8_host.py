@@ -109,7 +109,7 @@ def z(*shape, dtype=bf):
 
 def weight(N=64, K=256):
     w = mb.Fp8Weight.__new__(mb.Fp8Weight)   # the constructor wants GPU memory
-    w.N, w.K, w.device = N, K, torch.device("cpu")
+    w.N, w.K, w.index = N, K, -1
     w.codes, w.scale = z(N, K, dtype=f8), z(-(-N // 128), -(-K // 128), dtype=f32)
     w._ptrs = (w.codes.data_ptr(), w.scale.data_ptr())
     return w
@@ -164,7 +164,7 @@ def test_quantize_rejects():
 
 def test_block_rejects():
     e = mb.Fp8Experts.__new__(mb.Fp8Experts)
-    e.E, e.d, e.I, e.Is, e.device, e._ref = 8, 64, 32, 0, torch.device("cpu"), None
+    e.E, e.d, e.I, e.Is, e.index, e._ref = 8, 64, 32, 0, -1, None
     ok = dict(X=z(2, 64), Wr=z(8, 64), k=2, experts=e, out=z(2, 64), ws=z(1024, dtype=torch.uint8))
     with pytest.raises(ValueError, match="GPU memory"):
         mb.moe_block_fp8(**ok)

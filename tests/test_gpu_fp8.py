@@ -141,7 +141,8 @@ class Dense:
 
 SHAPES = [(1, 1, 16), (1, 7168, 2048), (2, 17, 48), (3, 130, 128), (4, 1001, 144), (5, 16, 7168), (7, 33, 1040), (8, 2304, 1040),
           (9, 130, 2048), (15, 20, 272), (16, 100, 7168), (17, 1001, 1040), (31, 48, 144), (32, 7, 2048), (33, 1001, 1040),
-          (48, 64, 272), (49, 130, 144), (63, 40, 8208), (64, 257, 2048), (64, 1, 16)]
+          (48, 64, 272), (49, 130, 144), (63, 40, 8208), (64, 257, 2048), (64, 1, 16), (20, 6408, 4112),
+          (40, 300, 4096)]
 
 
 @pytest.mark.parametrize("xt", ["bf16", "e4m3"])
