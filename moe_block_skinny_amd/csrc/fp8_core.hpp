@@ -84,16 +84,26 @@ __device__ __forceinline__ int x_load_token(int lane, int i) {
 template <int XK>
 constexpr int x_rows() { return (XK == XB || XK == X8) ? XTraits<XK>::kLoads : 1; }
 
+// Loads go through buffer descriptors: an offset past their end (kNoLoad and
+// more) reads zeros and asks nothing of memory, which is how rows, tokens and
+// columns that are not there are left out without a branch.
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+constexpr uint32_t kNoLoad = 0x80000000u;
+constexpr int kNonTemporal = 2;   // cache policy: weights are read once
+__device__ __forceinline__ buffer_t buffer_of(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
+}
+
 // Where a wave reads: per lane, byte offsets from uniform bases.
 template <int XK, int RT, int NT>
 struct Fp8Src {
-  const uint8_t* w[RT];     // tile's weight base (uniform)
-  uint32_t ra[RT], rb[RT];  // byte offset of row lane / 8 among the tile's rows 0-7, and among its rows 8-15
+  buffer_t w[RT];           // from the tile's weight base
+  uint32_t ra[RT], rb[RT];  // byte offset of row lane / 8 among the tile's rows 0-7, and among its rows 8-15, or kNoLoad
   const float* sa[RT];      // scales of the block row that holds the tile's row 0 (uniform), [blocks]
   const float* sb[RT];      // and of that of the rows of the upper lanes (row_b)
   bool row_b[RT];           // the lane's result rows take sb
-  const void* x;            // activations (uniform)
-  uint32_t xo[NT][x_rows<XK>()];   // byte offset of the token row of each load
+  buffer_t x;               // activations
+  uint32_t xo[NT][x_rows<XK>()];   // byte offset of the token row of each load, or kNoLoad
   const float* xs;          // e4m3: scales (uniform)
   uint32_t xso[NT];         // e4m3: index of the first scale of the lane's column's token
   int K;
@@ -151,50 +161,44 @@ struct Fp8Block {
   float xs[NT];
 };
 
-// Request block kb.  A block past the last is clamped to it (and must not be
-// used); in a short last block a lane past K re-reads the row's last columns.
+// Request block kb; what lies past K, all of a block past the last, is zeros.
 template <int XK, int RT, int NT>
 __device__ __forceinline__ void fp8_load(const Fp8Src<XK, RT, NT>& s, int kb, Fp8Block<XK, RT, NT>& r) {
   const int lane = s.lane, g = lane >> 4;
-  const int last = (s.K - 1) / kQBlock;
-  const uint32_t k0 = (uint32_t)(kb < last ? kb : last) * kQBlock;
-  const uint32_t K = (uint32_t)s.K;
-  auto below = [](uint32_t v, uint32_t top) { return v < top ? v : top; };
-  const char* x = reinterpret_cast<const char*>(s.x);
+  const uint32_t k0 = (uint32_t)kb * kQBlock, K = (uint32_t)s.K;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < XTraits<XK>::kLoads; ++i) {
-      uint32_t c;   // column of the lane's 16 bytes in the block
-      if constexpr (XK == XP4) c = 32 * g + 8 * (lane & 3);
-      else if constexpr (XK == XP8) c = 32 * g + 16 * i + 8 * (lane & 1);
-      else if constexpr (XK == XB) c = 8 * (lane & 15);
-      else if constexpr (XK == X8P) c = 32 * g + 16 * (lane & 1);
-      else c = 16 * (lane & 7);
-      const uint32_t o = s.xo[nt][x_rows<XK>() > 1 ? i : 0];
-      if constexpr (x_e4m3(XK)) r.x[nt][i] = ld128(x + (o + below(k0 + c, K - 16)));
-      else r.x[nt][i] = ld128(x + (o + 2 * below(k0 + c, K - 8)));
+      uint32_t c = k0;   // column of the lane's 16 bytes
+      if constexpr (XK == XP4) c += 32 * g + 8 * (lane & 3);
+      else if constexpr (XK == XP8) c += 32 * g + 16 * i + 8 * (lane & 1);
+      else if constexpr (XK == XB) c += 8 * (lane & 15);
+      else if constexpr (XK == X8P) c += 32 * g + 16 * (lane & 1);
+      else c += 16 * (lane & 7);
+      const uint32_t o = s.xo[nt][x_rows<XK>() > 1 ? i : 0] + (x_e4m3(XK) ? c : 2 * c);
+      r.x[nt][i] = __builtin_amdgcn_raw_buffer_load_b128(s.x, c < K ? o : kNoLoad, 0, 0);
     }
-    if constexpr (x_e4m3(XK)) r.xs[nt] = s.xs[s.xso[nt] + k0 / kQBlock];
+    if constexpr (x_e4m3(XK)) {
+      const uint32_t last = (K - 1) / kQBlock;
+      r.xs[nt] = s.xs[s.xso[nt] + ((uint32_t)kb < last ? (uint32_t)kb : last)];
+    }
   }
-  const uint32_t c = below(k0 + 16 * (lane & 7), K - 16);
+  const uint32_t c = k0 + 16 * (lane & 7);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    r.a[rt] = ld128_stream(s.w[rt] + (s.ra[rt] + c));
-    r.b[rt] = ld128_stream(s.w[rt] + (s.rb[rt] + c));
+    r.a[rt] = __builtin_amdgcn_raw_buffer_load_b128(s.w[rt], c < K ? s.ra[rt] + c : kNoLoad, 0, kNonTemporal);
+    r.b[rt] = __builtin_amdgcn_raw_buffer_load_b128(s.w[rt], c < K ? s.rb[rt] + c : kNoLoad, 0, kNonTemporal);
   }
 }
 
 // acc += the block's products, each tile's by its scale sc[rt].  lds: the
 // wave's buffer.
 template <int XK, int RT, int NT>
-__device__ __forceinline__ void fp8_block(int lane, const Fp8Block<XK, RT, NT>& r, const float (&sc)[RT], int kb, int K,
-                                          char* lds, f32x4 (&acc)[RT][NT]) {
-  const int g = lane >> 4;
+__device__ __forceinline__ void fp8_block(int lane, const Fp8Block<XK, RT, NT>& r, const float (&sc)[RT], char* lds,
+                                          f32x4 (&acc)[RT][NT]) {
   const u32x4 zero = {0u, 0u, 0u, 0u};
   const f32x4 fzero = {0.f, 0.f, 0.f, 0.f};
-  const bool tail = (kb + 1) * kQBlock > K;   // uniform: a short last block, zeros past K on both sides
-  const int c0 = kb * kQBlock + 32 * g;
   char* xl = lds + RT * 2048;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) rows128_store(lane, lds + rt * 2048, r.a[rt], r.b[rt]);
@@ -215,18 +219,6 @@ __device__ __forceinline__ void fp8_block(int lane, const Fp8Block<XK, RT, NT>& 
 #pragma unroll
       for (int i = 0; i < XTraits<XK>::kLoads; ++i) h[nt][i] = r.x[nt][i];
     }
-    if (tail) {   // zeros past K
-#pragma unroll
-      for (int i = 0; i < (XK == X8 ? 2 : XTraits<XK>::kLoads); ++i) {
-        int c;
-        if constexpr (XK == XP4) c = c0 + 8 * (lane & 3);
-        else if constexpr (XK == XP8) c = c0 + 16 * i + 8 * (lane & 1);
-        else if constexpr (XK == XB) c = c0 + 8 * i;
-        else if constexpr (XK == X8P) c = c0 + 16 * (lane & 1);
-        else c = c0 + 16 * i;
-        if (c >= K) h[nt][i] = zero;
-      }
-    }
   }
   auto x_step = [&](int nt, int j) {
     if constexpr (x_e4m3(XK)) {
@@ -246,10 +238,6 @@ __device__ __forceinline__ void fp8_block(int lane, const Fp8Block<XK, RT, NT>& 
   for (int rt = 0; rt < RT; ++rt) {
     u32x4 lo, hi;
     rows128_load(lane, lds + rt * 2048, lo, hi);
-    if (tail) {
-      if (c0 >= K) lo = zero;
-      if (c0 + 16 >= K) hi = zero;
-    }
     f32x4 d[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) d[nt] = fzero;
@@ -315,7 +303,7 @@ __device__ __forceinline__ void fp8_wave(const Fp8Src<XK, RT, NT>& s, int wave, 
     for (int u = 0; u < U; ++u) {
       float sc[RT];
       scale_of(sp, u, sc);
-      fp8_block<XK, RT, NT>(lane, r[u], sc, kb + u, s.K, lds, acc);   // every step but the last is whole
+      fp8_block<XK, RT, NT>(lane, r[u], sc, lds, acc);   // every step but the last is whole
       fp8_load<XK, RT, NT>(s, next + u, r[u]);
       __builtin_amdgcn_sched_barrier(0);   // a block's operands at a time (registers)
     }
@@ -326,7 +314,7 @@ __device__ __forceinline__ void fp8_wave(const Fp8Src<XK, RT, NT>& s, int wave, 
     if (kb + u < KB) {
       float sc[RT];
       scale_of(sv, u, sc);
-      fp8_block<XK, RT, NT>(lane, r[u], sc, kb + u, s.K, lds, acc);
+      fp8_block<XK, RT, NT>(lane, r[u], sc, lds, acc);
     }
     __builtin_amdgcn_sched_barrier(0);   // a block's operands at a time (registers)
   }

@@ -84,9 +84,9 @@ __device__ __forceinline__ uint32_t h_tile(const Fp8ExpertLaunch& a, const Fp8En
 
 // ---- gate/up + SwiGLU ----------------------------------------------------------
 //
-// A task is 8 pairs of an entry: a tile of 8 gate rows (p0 ..) and the 8 up
-// rows of the same pairs.  The waves split d by blocks and meet in LDS, where
-// the gate sum of a pair finds its up sum.
+// A task is 8 RT pairs of an entry: RT tiles of 8 gate rows (p0 ..) and the 8
+// up rows of the same pairs.  The waves split d by blocks and meet in LDS,
+// where the gate sum of a pair finds its up sum.
 
 constexpr int kFp8Pairs = 8;
 constexpr int kKeysMaxTokens = 2;
@@ -94,25 +94,28 @@ constexpr int kUpRouterWaves = 8;   // waves of a workgroup that scores router r
 constexpr int kUpU = 2;             // blocks in flight a wave, B <= 8 (4: the same time, 25 more registers)
 constexpr int kUpManyWaves = 4, kUpManyWgs = 2;   // B > 8: waves a workgroup, workgroups a compute unit (256 registers)
 
-template <int XK, int NT, int U, bool TILED>
+template <int XK, int RT, int NT, int U, bool TILED>
 __device__ __forceinline__ void up_fp8(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v, int p0,
                                        char* s_lds) {
-  constexpr int kWaveLds = fp8_wave_lds<XK, 1, NT>();
+  constexpr int kWaveLds = fp8_wave_lds<XK, RT, NT>();
   constexpr int TOK = XTraits<XK>::kTokens, COLS = XTraits<XK>::kCols;
   const int lane = own_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = (int)(blockDim.x >> 6);
   const int d = a.e.d, KB = (d + kQBlock - 1) / kQBlock, IB = (v.I + kQBlock - 1) / kQBlock;
-  Fp8Src<XK, 1, NT> s;
+  Fp8Src<XK, RT, NT> s;
   s.K = d;
   s.lane = lane;
-  s.x = a.e.X;
+  s.x = buffer_of(a.e.X);
   s.xs = nullptr;
-  s.w[0] = v.W13 + (size_t)p0 * d;
-  s.ra[0] = (uint32_t)(lane >> 3) * (uint32_t)d;   // I is a multiple of 8: no pair is past it
-  s.rb[0] = (uint32_t)(v.I + (lane >> 3)) * (uint32_t)d;
-  s.sa[0] = v.s13 + (size_t)(p0 / kQBlock) * KB;
-  s.sb[0] = v.s13 + (size_t)(IB + p0 / kQBlock) * KB;
-  s.row_b[0] = lane >= 32;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    s.w[rt] = buffer_of(v.W13 + (size_t)(p0 + 8 * rt) * d);
+    s.ra[rt] = (uint32_t)(lane >> 3) * (uint32_t)d;   // I is a multiple of 16: no pair is past it
+    s.rb[rt] = (uint32_t)(v.I + (lane >> 3)) * (uint32_t)d;
+    s.sa[rt] = v.s13 + (size_t)(p0 / kQBlock) * KB;
+    s.sb[rt] = v.s13 + (size_t)(IB + p0 / kQBlock) * KB;
+    s.row_b[rt] = lane >= 32;
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -120,21 +123,23 @@ __device__ __forceinline__ void up_fp8(const Fp8ExpertLaunch& a, const int32_t* 
       const int t = nt * TOK + x_load_token<XK>(lane, i);
       int tok, sr;
       fp8_token(a, s_plan, v, t < v.m ? t : v.m - 1, tok, sr);
-      s.xo[nt][i] = (uint32_t)tok * (uint32_t)d * 2;
+      s.xo[nt][i] = t < v.m ? (uint32_t)tok * (uint32_t)d * 2 : kNoLoad;
     }
     s.xso[nt] = 0;
   }
-  f32x4 acc[1][NT];
-  fp8_wave<XK, 1, NT, U>(s, wave, waves, s_lds + wave * kWaveLds, acc);
+  f32x4 acc[RT][NT];
+  fp8_wave<XK, RT, NT, U>(s, wave, waves, s_lds + wave * kWaveLds, acc);
   f32x4* mine = reinterpret_cast<f32x4*>(s_lds + wave * kWaveLds);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) mine[nt * 64 + lane] = acc[0][nt];
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mine[(rt * NT + nt) * 64 + lane] = acc[rt][nt];
   lds_barrier();
-  for (int i = threadIdx.x; i < NT * 32; i += (int)blockDim.x) {
-    const int l = i & 31, nt = i >> 5, col = l & 15;
+  for (int i = threadIdx.x; i < RT * NT * 32; i += (int)blockDim.x) {
+    const int l = i & 31, rt = (i >> 5) / NT, nt = (i >> 5) % NT, col = l & 15;
     const int t = nt * TOK + col / COLS;
     if (col % COLS || t >= v.m) continue;
-    const f32x4* sum = reinterpret_cast<const f32x4*>(s_lds) + nt * 64 + l;
+    const f32x4* sum = reinterpret_cast<const f32x4*>(s_lds) + (i >> 5) * 64 + l;
     f32x4 g = sum[0], u = sum[32];
     for (int w = 1; w < waves; ++w) {
       g += sum[w * (kWaveLds / 16)];
@@ -145,50 +150,51 @@ __device__ __forceinline__ void up_fp8(const Fp8ExpertLaunch& a, const int32_t* 
     for (int q = 0; q < 4; ++q) h[q] = silu(g[q]) * u[q];
     int tok, sr;
     fp8_token(a, s_plan, v, t, tok, sr);
-    u32x2 hi, lo;
     uint32_t h0, l0, h1, l1;
     split_bf16x2(h[0], h[1], h0, l0);
     split_bf16x2(h[2], h[3], h1, l1);
-    hi = u32x2{h0, h1};
-    lo = u32x2{l0, l1};
-    const int i0 = p0 + 4 * (l >> 4);
+    const int i0 = p0 + 8 * rt + 4 * (l >> 4);
     if constexpr (TILED) {
       const size_t o = (size_t)h_tile(a, v, t) + (i0 >> 7) * 2048 + ((i0 >> 3) & 3) * 512 + ((i0 >> 5) & 3) * 128 + (t & 15) * 8 + (i0 & 7);
-      *reinterpret_cast<u32x2*>(a.e.ht_hi + o) = hi;
-      *reinterpret_cast<u32x2*>(a.e.ht_lo + o) = lo;
+      *reinterpret_cast<u32x2*>(a.e.ht_hi + o) = u32x2{h0, h1};
+      *reinterpret_cast<u32x2*>(a.e.ht_lo + o) = u32x2{l0, l1};
     } else {
       const size_t o = (size_t)sr * a.e.hld + i0;
-      *reinterpret_cast<u32x2*>(h_hi(a.e) + o) = hi;
-      *reinterpret_cast<u32x2*>(h_lo(a.e) + o) = lo;
+      *reinterpret_cast<u32x2*>(h_hi(a.e) + o) = u32x2{h0, h1};
+      *reinterpret_cast<u32x2*>(h_lo(a.e) + o) = u32x2{l0, l1};
     }
   }
   lds_barrier();   // the buffers are free for the next task
 }
 
-// MAXB: the largest batch of the instantiation (4, 8 or 64).
+// A task of 8 pairs of an entry of at most 16 tokens.  MAXB: the largest
+// batch of the instantiation (4, 8 or 64).
 template <int MAXB>
-__device__ __forceinline__ void up_fp8_dispatch(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v,
-                                                int p0, char* s_lds) {
-  if constexpr (MAXB <= 4) {
-    up_fp8<XP4, 1, kUpU, false>(a, s_plan, v, p0, s_lds);
-  } else if constexpr (MAXB <= 8) {
-    if (v.m <= 4) up_fp8<XP4, 1, kUpU, false>(a, s_plan, v, p0, s_lds);
-    else up_fp8<XP8, 1, kUpU, false>(a, s_plan, v, p0, s_lds);
-  } else {
-    const int nt = (v.m + 15) / 16;
-    if (v.m <= 4) up_fp8<XP4, 1, 4, true>(a, s_plan, v, p0, s_lds);
-    else if (v.m <= 8) up_fp8<XP8, 1, 4, true>(a, s_plan, v, p0, s_lds);
-    else if (nt <= 1) up_fp8<XB, 1, 4, true>(a, s_plan, v, p0, s_lds);
-    else if (nt == 2) up_fp8<XB, 2, 2, true>(a, s_plan, v, p0, s_lds);
-    else if (nt == 3) up_fp8<XB, 3, 1, true>(a, s_plan, v, p0, s_lds);
-    else up_fp8<XB, 4, 1, true>(a, s_plan, v, p0, s_lds);
+__device__ __forceinline__ void up_fp8_light(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v, int p0,
+                                             char* s_lds) {
+  constexpr bool MANY = MAXB > 8;
+  constexpr int U = MANY ? 4 : kUpU;
+  if (MAXB <= 4 || v.m <= 4) {
+    up_fp8<XP4, 1, 1, U, MANY>(a, s_plan, v, p0, s_lds);
+  } else if constexpr (MAXB > 4) {
+    if (!MANY || v.m <= 8) up_fp8<XP8, 1, 1, U, MANY>(a, s_plan, v, p0, s_lds);
+    else if constexpr (MANY) up_fp8<XB, 1, 1, U, MANY>(a, s_plan, v, p0, s_lds);
   }
+}
+
+// A task of 16 pairs of an entry of more than 16 tokens: its activations, four
+// to eight times a tile's weight bytes, are read half as often as for 8.
+__device__ __forceinline__ void up_fp8_heavy(const Fp8ExpertLaunch& a, const int32_t* s_plan, const Fp8Entry& v, int p0,
+                                             char* s_lds) {
+  if (v.m <= 32) up_fp8<XB, 2, 2, 2, true>(a, s_plan, v, p0, s_lds);
+  else if (v.m <= 48) up_fp8<XB, 2, 3, 1, true>(a, s_plan, v, p0, s_lds);
+  else up_fp8<XB, 2, 4, 1, true>(a, s_plan, v, p0, s_lds);
 }
 
 // Waves of a workgroup: at most 16 of 128 registers (B <= 8), or 4 of 256.
 template <int MAXB> struct UpFp8 {
   static constexpr int kWaves = MAXB <= 8 ? 16 : kUpManyWaves;
-  static constexpr int kWaveLds = MAXB <= 4 ? fp8_wave_lds<XP4, 1, 1>() : MAXB <= 8 ? fp8_wave_lds<XP8, 1, 1>() : fp8_wave_lds<XB, 1, 4>();
+  static constexpr int kWaveLds = MAXB <= 4 ? fp8_wave_lds<XP4, 1, 1>() : MAXB <= 8 ? fp8_wave_lds<XP8, 1, 1>() : fp8_wave_lds<XB, 2, 4>();
 };
 
 template <int MAXB>
@@ -196,14 +202,13 @@ __global__ __launch_bounds__(UpFp8<MAXB>::kWaves * 64, MAXB <= 8 ? 1 : kUpManyWg
   __shared__ int32_t s_plan[kMaxPlanWords];
   extern __shared__ __align__(16) char s_lds[];   // a buffer per wave; first plan_from_ids' scratch
   const ExpertLaunch& x = a.e;
-  const int tiles_r = x.I / kFp8Pairs;
-  const int tiles_s = x.Ws13 ? x.Is / kFp8Pairs : 0;
   // where the tokens are selected here: without ready words at most two of
   // them, a wave each
   __shared__ TopkScratch s_tk[MAXB <= 8 ? kKeysMaxTokens : 1];
   __shared__ int32_t s_ids[64];
   __shared__ float s_w[64];
   __shared__ int s_order[MAXB > 8 ? kMaxB * kMaxK + kMaxB : 1];
+  __shared__ int s_heavy[3];
   if constexpr (MAXB <= 4) {
     // With the router rows in this launch, its first router_wgs workgroups
     // score them and leave
@@ -218,46 +223,93 @@ __global__ __launch_bounds__(UpFp8<MAXB>::kWaves * 64, MAXB <= 8 ? 1 : kUpManyWg
     if (x.ready) select_own_token(x, s_tk, s_ids, s_w);
   }
   const int G = (int)gridDim.x - x.router_wgs, wg = (int)blockIdx.x - x.router_wgs;
-  // Tasks: the shared expert's tiles, then the routed entries'.  Where the
-  // tokens are selected here the shared tiles, which need no plan, stream
-  // meanwhile (a loop of its own: one loop over both, with the routing inside
-  // it, spilled 24 registers).  Beyond 8 tokens the entries come by falling
-  // token count, and every other round of the workgroups goes backwards, so
-  // that who had a long task first has a short one next.
-  int task = wg;
   if constexpr (MAXB <= 8) {
+    // Tasks of 8 pairs: the shared expert's, then the routed entries'.  Where
+    // the tokens are selected here the shared tiles, which need no plan,
+    // stream meanwhile (a loop of its own: one loop over both, with the
+    // routing inside it, spilled 24 registers).
+    const int tiles_r = x.I / kFp8Pairs, tiles_s = x.Ws13 ? x.Is / kFp8Pairs : 0;
+    int task = wg;
     if (x.logits || x.lkeys) {
-      for (; task < tiles_s; task += G) {
-        const Fp8Entry v = fp8_entry(a, s_plan, -1, 0);
-        up_fp8_dispatch<MAXB>(a, s_plan, v, task * kFp8Pairs, s_lds);
-      }
+      for (; task < tiles_s; task += G)
+        up_fp8_light<MAXB>(a, s_plan, fp8_entry(a, s_plan, -1, 0), task * kFp8Pairs, s_lds);
       if (x.ready) wait_token_plan(x, s_plan, s_tk, s_ids);
       else route_here<false, 1>(x, s_plan, s_tk, s_ids, s_w);
     } else {
       stage_plan(x, s_plan);
     }
+    const int n = wave_uniform(s_plan[0]), total = tiles_s + n * tiles_r;
+    for (; task < total; task += G) {
+      const int idx = task < tiles_s ? n : (task - tiles_s) / tiles_r;
+      const int tile = task < tiles_s ? task : task - tiles_s - idx * tiles_r;
+      up_fp8_light<MAXB>(a, s_plan, fp8_entry(a, s_plan, n, idx), tile * kFp8Pairs, s_lds);
+    }
   } else {
+    // Heavy tasks (entries of more than 16 tokens, the shared expert's first,
+    // then by falling token tiles: 16 pairs each) go one to a workgroup, then
+    // the light ones (8 pairs) so that the workgroups' costs come out even:
+    // measured, a task of 2, 3 or 4 token tiles takes as long as 2, 3 or 4
+    // light ones.  Round r of the light tasks goes to the workgroups, last[r]
+    // on, that have room for more than r of them; tiles that lie next to each
+    // other are read at the same time.  (In turns, forwards and backwards,
+    // the workgroups with heavy tasks ended 15 us after the others in the
+    // batch-64 workload: gate/up 52.6 us.)
     const PlanView p = x.ids_in ? plan_from_ids(x, s_plan, reinterpret_cast<unsigned char*>(s_lds)) : stage_plan(x, s_plan);
-    if (threadIdx.x < 64) order_entries_by_tiles(x, p, p.n, s_order);
+    const int n = wave_uniform(s_plan[0]);
+    if (threadIdx.x < 64) {
+      order_entries_by_tiles(x, p, n, s_order);
+      int c2 = 0, c3 = 0, c4 = 0;   // entries of at least 2, 3, 4 token tiles
+      for (int e0 = 0; e0 < n; e0 += 64) {
+        const int e = e0 + (int)threadIdx.x, m = e < n ? p.offs[e + 1] - p.offs[e] : 0;
+        c2 += __popcll(__ballot(m > 16));
+        c3 += __popcll(__ballot(m > 32));
+        c4 += __popcll(__ballot(m > 48));
+      }
+      if (threadIdx.x == 0) {
+        s_heavy[0] = c2;
+        s_heavy[1] = c3;
+        s_heavy[2] = c4;
+      }
+    }
     __syncthreads();
-  }
-  const int n = wave_uniform(s_plan[0]), total = tiles_s + n * tiles_r;
-  for (int round = 0;; ++round, task += G) {
-    if constexpr (MAXB > 8) {
-      if (round * G >= total) break;
-      task = round * G + ((round & 1) ? G - 1 - wg : wg);
-      if (task >= total) continue;
-    } else {
-      if (task >= total) break;
+    const int c2 = wave_uniform(s_heavy[0]), c3 = wave_uniform(s_heavy[1]), c4 = wave_uniform(s_heavy[2]);
+    const int th = x.I / (2 * kFp8Pairs), tl = x.I / kFp8Pairs;
+    const int sh = x.Ws13 && x.B > 16 ? x.Is / (2 * kFp8Pairs) : 0, slt = x.Ws13 && x.B <= 16 ? x.Is / kFp8Pairs : 0;
+    // heavy tasks of at least 2, 3, 4 token tiles
+    const int h2 = c2 * th + sh, h3 = c3 * th + (x.B > 32 ? sh : 0), h4 = c4 * th + (x.B > 48 ? sh : 0);
+    for (int task = wg; task < h2; task += G) {
+      int idx = n, tile = task;
+      if (task >= sh) {
+        const int q = (task - sh) / th;
+        idx = wave_uniform(s_order[q]);
+        tile = task - sh - q * th;
+      }
+      up_fp8_heavy(a, s_plan, fp8_entry(a, s_plan, n, idx), tile * 2 * kFp8Pairs, s_lds);
     }
-    int idx = n, tile = task;   // the shared expert
-    if (task >= tiles_s) {
-      idx = (task - tiles_s) / tiles_r;
-      tile = task - tiles_s - idx * tiles_r;
-      if (MAXB > 8) idx = wave_uniform(s_order[idx]);
+    const int light = slt + (n - c2) * tl;
+    auto clip = [&](int h) { return h < G ? h : G; };   // more heavy tasks than workgroups: every one has had some
+    const int g2 = h2 > G ? 0 : h2, g3 = h2 > G ? 0 : clip(h3), g4 = h2 > G ? 0 : clip(h4);
+    // the fewest rounds with room for all of them
+    int T = 1;
+    auto room = [&](int T) {
+      auto pos = [](int v) { return v > 0 ? v : 0; };
+      return g4 * pos(T - 4) + (g3 - g4) * pos(T - 3) + (g2 - g3) * pos(T - 2) + (G - g2) * T;
+    };
+    while (room(T) < light && T < 1024) ++T;
+    int base = 0;
+    for (int r = 0; r < T; ++r) {
+      const int first = T - 4 > r ? 0 : (T - 3 > r ? g4 : (T - 2 > r ? g3 : g2));
+      const int task = base + wg - first;
+      base += G - first;
+      if (wg < first || task >= light) continue;
+      int idx = n, tile = task;
+      if (task >= slt) {
+        const int q = (task - slt) / tl;
+        idx = wave_uniform(s_order[c2 + q]);
+        tile = task - slt - q * tl;
+      }
+      up_fp8_light<MAXB>(a, s_plan, fp8_entry(a, s_plan, n, idx), tile * kFp8Pairs, s_lds);
     }
-    const Fp8Entry v = fp8_entry(a, s_plan, n, idx);
-    up_fp8_dispatch<MAXB>(a, s_plan, v, tile * kFp8Pairs, s_lds);
   }
 }
 

@@ -214,26 +214,28 @@ __global__ __launch_bounds__(MAXW * 64) void gemm_fp8_kernel(GemmFp8Launch a) {
   Fp8Src<XK, RT, NT> s;
   s.K = a.K;
   s.lane = lane;
-  s.x = a.X;
+  s.x = buffer_of(a.X);
   s.xs = a.Xs;
   const int xb = x_e4m3(XK) ? 1 : 2;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    // rows past N re-read the last one and are not stored
     const int base = r0 + 16 * rt < a.N ? r0 + 16 * rt : a.N - 1;
-    const int ra = base + (lane >> 3), rb = ra + 8;
-    s.w[rt] = a.W + (size_t)base * a.K;
-    s.ra[rt] = (uint32_t)((ra < a.N ? ra : a.N - 1) - base) * (uint32_t)a.K;
-    s.rb[rt] = (uint32_t)((rb < a.N ? rb : a.N - 1) - base) * (uint32_t)a.K;
+    const int ra = r0 + 16 * rt + (lane >> 3), rb = ra + 8;
+    s.w[rt] = buffer_of(a.W + (size_t)base * a.K);
+    s.ra[rt] = ra < a.N ? (uint32_t)(ra - base) * (uint32_t)a.K : kNoLoad;
+    s.rb[rt] = rb < a.N ? (uint32_t)(rb - base) * (uint32_t)a.K : kNoLoad;
     s.sa[rt] = s.sb[rt] = a.Ws + (size_t)(base / kQBlock) * KB;   // a tile of 16 rows lies in one block row
     s.row_b[rt] = false;
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    auto token = [&](int t) { return (uint32_t)(nt * TOK + t < a.M ? nt * TOK + t : a.M - 1); };
 #pragma unroll
-    for (int i = 0; i < x_rows<XK>(); ++i) s.xo[nt][i] = token(x_load_token<XK>(lane, i)) * (uint32_t)a.K * xb;
-    s.xso[nt] = token(x_column_token<XK>(lane)) * (uint32_t)KB;
+    for (int i = 0; i < x_rows<XK>(); ++i) {
+      const int t = nt * TOK + x_load_token<XK>(lane, i);
+      s.xo[nt][i] = t < a.M ? (uint32_t)t * (uint32_t)a.K * xb : kNoLoad;
+    }
+    const int t = nt * TOK + x_column_token<XK>(lane);
+    s.xso[nt] = (uint32_t)(t < a.M ? t : a.M - 1) * (uint32_t)KB;
   }
   f32x4 acc[RT][NT];
   fp8_wave<XK, RT, NT, U>(s, wave, waves, s_lds + wave * kWaveLds, acc);
