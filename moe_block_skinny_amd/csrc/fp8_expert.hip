@@ -77,7 +77,10 @@ __device__ __forceinline__ void fp8_token(const Fp8ExpertLaunch& a, const int32_
 //   t its 8 values -- one contiguous load per step.  From slot rows, lanes of
 //   different tokens in every quad, the same loads take a compute unit 3.5
 //   times as long (37 against 130 bytes/ns), and h crosses once per
-//   workgroup.
+//   workgroup.  An entry of up to kRowTokens tokens keeps plain rows in its
+//   tile all the same: a tile's steps would bring in a cache line for every
+//   16 bytes of a lone token.
+constexpr int kRowTokens = 4;
 __device__ __forceinline__ uint32_t h_tile(const Fp8ExpertLaunch& a, const Fp8Entry& v, int t) {
   return (uint32_t)(v.hbase + (t & ~15)) * (uint32_t)a.e.hld;
 }
@@ -155,7 +158,7 @@ __device__ __forceinline__ void up_fp8(const Fp8ExpertLaunch& a, const int32_t* 
     split_bf16x2(h[2], h[3], h1, l1);
     const int i0 = p0 + 8 * rt + 4 * (l >> 4);
     if constexpr (TILED) {
-      const size_t o = (size_t)h_tile(a, v, t) + (i0 >> 7) * 2048 + ((i0 >> 3) & 3) * 512 + ((i0 >> 5) & 3) * 128 + (t & 15) * 8 + (i0 & 7);
+      const size_t o = v.m <= kRowTokens ? (size_t)(v.hbase + t) * a.e.hld + i0 : (size_t)h_tile(a, v, t) + (i0 >> 7) * 2048 + ((i0 >> 3) & 3) * 512 + ((i0 >> 5) & 3) * 128 + (t & 15) * 8 + (i0 & 7);
       *reinterpret_cast<u32x2*>(a.e.ht_hi + o) = u32x2{h0, h1};
       *reinterpret_cast<u32x2*>(a.e.ht_lo + o) = u32x2{l0, l1};
     } else {
@@ -344,20 +347,25 @@ struct DownFp8 {
   // token tile at t0: h operands
   __device__ __forceinline__ void load_h(const Fp8Entry& v, int t0, DownH<KBM>& h) const {
     const int lane = threadIdx.x & 63, g = lane >> 4, t = t0 + (lane & 15);
+    const bool tiled = TILED && v.m > kRowTokens;   // uniform
     uint32_t base;
-    if constexpr (TILED) {
+    if (tiled) {
       base = h_tile(a, v, t0) * 2 + lane * 16;
     } else {
-      int tok, sr;
-      fp8_token(a, s_plan, v, t < v.m ? t : v.m - 1, tok, sr);
-      base = (uint32_t)sr * (uint32_t)a.e.hld * 2 + 64 * g;
+      int row = v.hbase + t;
+      if constexpr (!TILED) {
+        int tok;
+        fp8_token(a, s_plan, v, t < v.m ? t : v.m - 1, tok, row);
+      }
+      base = (uint32_t)row * (uint32_t)a.e.hld * 2 + 64 * g;
     }
+    const uint32_t per_kb = tiled ? 4096 : 256, per_j = tiled ? 1024 : 16;
 #pragma unroll
     for (int kb = 0; kb < KBM; ++kb)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool ok = t < v.m && kb * kQBlock + 32 * g + 8 * j < v.I;
-        const uint32_t o = ok ? base + (TILED ? kb * 4096 + j * 1024 : kb * 256 + 16 * j) : 0xfffffff0u;
+        const uint32_t o = ok ? base + kb * per_kb + j * per_j : kNoLoad;
         h.hv[kb][j] = __builtin_amdgcn_raw_buffer_load_b128(hi, o, 0, 0);
         h.lv[kb][j] = __builtin_amdgcn_raw_buffer_load_b128(lo, o, 0, 0);
       }
@@ -463,7 +471,8 @@ __global__ __launch_bounds__(DownWaves<KBM>::kMax * 64) void expert_down_combine
   const PlanView p = stage_plan(x, s_plan);
   const int n = wave_uniform(p.n), ne = n + (x.Ws13 ? 1 : 0);
   if (wave == 0) {
-    order_entries_by_tiles(x, p, ne, s_order);
+    // up to 16 tokens every entry has one token tile: any order will do
+    if (x.B > 16) order_entries_by_tiles(x, p, ne, s_order);
     if ((threadIdx.x & 63) == 0) s_next = nw;
   }
   __syncthreads();
@@ -480,7 +489,7 @@ __global__ __launch_bounds__(DownWaves<KBM>::kMax * 64) void expert_down_combine
     if ((threadIdx.x & 63) == 0) u = atomicAdd(&s_next, 1);
     return wave_uniform(u);
   };
-  auto entry = [&](int u) { return fp8_entry(a, s_plan, n, wave_uniform(s_order[u])); };
+  auto entry = [&](int u) { return fp8_entry(a, s_plan, n, x.B > 16 ? wave_uniform(s_order[u]) : u); };
   if (wave < ne) {
     // The current entry's rows go to the wave's buffer as they arrive, which
     // frees their registers for the next entry's; its h is requested before

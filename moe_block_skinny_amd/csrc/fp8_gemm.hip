@@ -175,29 +175,35 @@ hipError_t launch_quantize(const QuantizeLaunch& a0, hipStream_t st) {
 // A workgroup owns 16 RT rows of W over all of K; its waves split K by blocks
 // and meet once, in LDS, in wave order (deterministic).
 
-// Results of tokens t, rows n .. n + 3 (only those below N are there).
-__device__ __forceinline__ void store_rows(const GemmFp8Launch& a, int t, int n, f32x4 v) {
+// Results of token t, rows n .. n + 3 (only those below N are there): with N a
+// multiple of 4 one store, r the residual's 4 bf16 (zeros without one).
+__device__ __forceinline__ u32x2 load_residual4(const GemmFp8Launch& a, int t, int n) {
+  if (!a.R) return u32x2{0u, 0u};
+  return *reinterpret_cast<const u32x2*>(a.R + (size_t)t * a.N + n);
+}
+__device__ __forceinline__ void store_rows4(const GemmFp8Launch& a, int t, int n, f32x4 v, u32x2 r) {
   const size_t o = (size_t)t * a.N + n;
-  if ((a.N & 3) == 0) {
-    if (a.R) {
-      const u32x2 r = *reinterpret_cast<const u32x2*>(a.R + o);
-      v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
-    }
-    if (a.y_bf16) {
-      const u32x2 p = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                       (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
-      *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(a.Y) + o) = p;
-    } else {
-      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.Y) + o) = v;
-    }
+  if (a.R) v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
+  if (a.y_bf16) {
+    const u32x2 p = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                     (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+    *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(a.Y) + o) = p;
   } else {
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.Y) + o) = v;
+  }
+}
+__device__ __forceinline__ void store_rows(const GemmFp8Launch& a, int t, int n, f32x4 v) {
+  if ((a.N & 3) == 0) {
+    store_rows4(a, t, n, v, load_residual4(a, t, n));
+    return;
+  }
+  const size_t o = (size_t)t * a.N + n;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (n + q >= a.N) break;
-      const float y = a.R ? v[q] + bf16_to_f32(a.R[o + q]) : v[q];
-      if (a.y_bf16) reinterpret_cast<bf16_t*>(a.Y)[o + q] = f32_to_bf16(y);
-      else reinterpret_cast<float*>(a.Y)[o + q] = y;
-    }
+  for (int q = 0; q < 4; ++q) {
+    if (n + q >= a.N) break;
+    const float y = a.R ? v[q] + bf16_to_f32(a.R[o + q]) : v[q];
+    if (a.y_bf16) reinterpret_cast<bf16_t*>(a.Y)[o + q] = f32_to_bf16(y);
+    else reinterpret_cast<float*>(a.Y)[o + q] = y;
   }
 }
 
@@ -315,6 +321,21 @@ __global__ __launch_bounds__(kSharedWaves * 64) void gemm_fp8_shared_kernel(Gemm
         mine[(rt * NT + nt) * 64] = acc[rt][nt];
       }
   }
+  // the eight waves share the pieces
+  constexpr int kPer = (kPieces + kSharedWaves - 1) / kSharedWaves, kSlices = 4;
+  auto piece = [&](int p) { return wave + kSharedWaves * p; };
+  auto token_of_piece = [&](int i) { return 16 * (i % NT) + (lane & 15); };
+  auto row_of_piece = [&](int i) { return (tile * 4 * RT + i / NT) * 16 + 4 * (lane >> 4); };
+  auto there = [&](int i) { return i < kPieces && token_of_piece(i) < a.M && row_of_piece(i) < a.N; };
+  const bool wide = (a.N & 3) == 0;
+  f32x4 v[kPer];
+  u32x2 res[kPer];
+  // the residual is requested ahead of what it is added to
+  auto request_residual = [&] {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+      res[p] = wide && there(piece(p)) ? load_residual4(a, token_of_piece(piece(p)), row_of_piece(piece(p))) : u32x2{0u, 0u};
+  };
   if (a.ks_n > 1) {
     const coherent_rsrc_t prs = coherent_rsrc(a.part);
     auto off = [&](int slice, int i) { return (uint32_t)((((tile * a.ks_n + slice) * kPieces + i) * 64 + lane) * 16); };
@@ -327,9 +348,8 @@ __global__ __launch_bounds__(kSharedWaves * 64) void gemm_fp8_shared_kernel(Gemm
     }
     __shared__ int s_last;
     if (!arrive_last(a.counter + tile, (uint32_t)a.ks_n, &s_last)) return;
-    // the eight waves share the pieces; kSlices slices are requested at a time
-    constexpr int kPer = (kPieces + kSharedWaves - 1) / kSharedWaves, kSlices = 4;
-    f32x4 v[kPer];
+    // kSlices slices are requested at a time
+    request_residual();
 #pragma unroll
     for (int p = 0; p < kPer; ++p) v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int q0 = 0; q0 < a.ks_n; q0 += kSlices) {
@@ -337,27 +357,26 @@ __global__ __launch_bounds__(kSharedWaves * 64) void gemm_fp8_shared_kernel(Gemm
 #pragma unroll
       for (int q = 0; q < kSlices; ++q)
 #pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-          const int i = wave + kSharedWaves * p;
-          pv[q][p] = ld_coherent4(prs, off(q0 + q < a.ks_n ? q0 + q : q0, i < kPieces ? i : 0));
-        }
+        for (int p = 0; p < kPer; ++p)
+          pv[q][p] = ld_coherent4(prs, off(q0 + q < a.ks_n ? q0 + q : q0, piece(p) < kPieces ? piece(p) : 0));
 #pragma unroll
       for (int q = 0; q < kSlices; ++q)
 #pragma unroll
         for (int p = 0; p < kPer; ++p)
           if (q0 + q < a.ks_n) v[p] += __builtin_bit_cast(f32x4, pv[q][p]);
     }
+  } else {
+    request_residual();
+    __syncthreads();
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int i = wave + kSharedWaves * p;
-      if (i < kPieces) sums[i * 64 + lane] = v[p];
-    }
+    for (int p = 0; p < kPer; ++p) v[p] = sums[(piece(p) < kPieces ? piece(p) : 0) * 64 + lane];
   }
-  __syncthreads();
-#pragma unroll 1
-  for (int i = wave; i < kPieces; i += kSharedWaves) {
-    const int t = 16 * (i % NT) + (lane & 15), row = (tile * 4 * RT + i / NT) * 16 + 4 * (lane >> 4);
-    if (t < a.M && row < a.N) store_rows(a, t, row, sums[i * 64 + lane]);
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int i = piece(p);
+    if (!there(i)) continue;
+    if (wide) store_rows4(a, token_of_piece(i), row_of_piece(i), v[p], res[p]);
+    else store_rows(a, token_of_piece(i), row_of_piece(i), v[p]);
   }
 }
 
