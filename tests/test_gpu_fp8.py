@@ -409,3 +409,191 @@ def test_graph_replays_of_the_whole_run(B):
     X8 = ref.VALUES[q[0]] * np.repeat(s[0], 128, axis=1)
     Y = X8 @ g.W64.T + g.X64
     assert np.abs(host(H) - Y).max() <= 2.0 ** -8 * np.abs(Y).max() + 1e-4 * rms(Y)
+
+
+# ---- ends of the ranges, and calls beside each other --------------------------------
+
+
+@pytest.mark.parametrize("xt,B", [("bf16", 2), ("e4m3", 6), ("bf16", 12), ("e4m3", 64), ("bf16", 64)])
+def test_gemm_longest_rows(xt, B):
+    c = Dense(B, 70, 65536, xt, seed=7)
+    Y = Guarded((B, 70), torch.float32)
+    c.call(Y.t)
+    c.check(host(Y.t), False, "f32")
+    Y.check()
+
+
+@pytest.mark.parametrize("B", [1, 20])
+def test_gemm_weight_past_4_gib(B):
+    """Rows beyond 2^32 bytes of the weight: zeros but for the first and the last block row."""
+    N, K = 66049, 65536
+    W = torch.zeros((N, K), dtype=torch.uint8, device="cuda")
+    r = rng(8, B)
+    rows = np.r_[0:3, N - 65:N]
+    codes = ref.encode(np.clip(r.standard_normal((len(rows), K)) * 107, -448, 448))
+    W[torch.from_numpy(rows).cuda()] = torch.from_numpy(codes).cuda()
+    S = torch.full((ref.blocks(N), ref.blocks(K)), 2.0 ** -14, device="cuda")
+    S[-1] = 2.0 ** -13
+    X = bf16(r.standard_normal((B, K)))
+    need = mb.workspace_bytes(mb.OP_SKINNY_GEMM_FP8, mb.DT_BF16, B=B, N=N, K=K)
+    Y = torch.empty((B, N), dtype=torch.float32, device="cuda")
+    mb.skinny_gemm_fp8(dev(X), mb.Fp8Weight(W.view(F8), S), Y, ws=mb.workspace(need) if need else None)
+    y = host(Y)
+    last = (N - 1) // 128 * 128
+    scale = np.where(rows < last, 2.0 ** -14, 2.0 ** -13)
+    W64 = ref.VALUES[codes] * scale[:, None]
+    want, sums = widen(X) @ W64.T, np.abs(widen(X)) @ np.abs(W64).T
+    assert (np.abs(y[:, rows] - want) <= (2.0 * (K + 2) + 1) * 2.0 ** -24 * sums).all()
+    y[:, rows] = 0
+    assert not y.any()
+
+
+@pytest.mark.parametrize("layout", ["rows", "blocks"])
+def test_quantize_past_4_gib(layout):
+    rows, cols = 66049, 65536
+    X = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    tail = hard_values(rng(9), 1, 129, cols)
+    th = bf16(tail)[0]
+    X[rows - 129:] = dev(th)
+    Q = torch.empty((rows, cols), dtype=F8, device="cuda")
+    S = torch.empty((rows if layout == "rows" else ref.blocks(rows), ref.blocks(cols)), device="cuda")
+    mb.moe_quantize_fp8(X, Q, S, layout)
+    # the last 128-row block starts at row 66048, one row before the end; the 128 rows ahead of it are one block
+    q, s = ref.quantize(widen(th)[None], layout)
+    if layout == "blocks":
+        q1, s1 = ref.quantize(widen(th[:128])[None], layout)
+        q2, s2 = ref.quantize(widen(th[128:])[None], layout)
+        q, s = np.concatenate([q1, q2], axis=1), np.concatenate([s1, s2], axis=1)
+    assert np.array_equal(codes_of(Q[rows - 129:]), q[0])
+    assert np.array_equal(host(S[-s.shape[1]:]), s[0])
+    assert not Q[: rows - 129].view(torch.uint8).any() and bool((S[: S.shape[0] - s.shape[1]] == 1).all())
+
+
+@pytest.mark.parametrize("B", [3, 20])
+def test_block_experts_past_4_gib_and_widest_hidden_size(B):
+    """d = 65536, and W13 of more than 2^32 bytes with the last expert chosen by every token."""
+    d, E, k, I = 65536, 130, 2, 256
+    r = rng(10, B)
+    g = torch.Generator(device="cuda").manual_seed(B)
+    code = lambda *s: torch.randint(0, 0x70, s, generator=g, device="cuda", dtype=torch.uint8)   # noqa: E731
+    W13, W2 = code(E, 2 * I, d), code(E, d, I)
+    s13 = torch.full((E, 2 * ref.blocks(I), ref.blocks(d)), 2.0 ** -14, device="cuda")
+    s2 = torch.full((E, ref.blocks(d), ref.blocks(I)), 2.0 ** -10, device="cuda")
+    X = bf16(r.standard_normal((B, d)))
+    Wr = bf16(r.standard_normal((E, d)) * d ** -0.5)
+    bias = np.zeros(E, np.float32)
+    bias[[5, E - 1]] = 50.0
+    out = torch.empty((B, d), dtype=torch.bfloat16, device="cuda")
+    ids = torch.empty((B, k), dtype=torch.int32, device="cuda")
+    ws = mb.workspace(mb.workspace_bytes(mb.OP_BLOCK_FP8, mb.DT_BF16, B=B, d=d, E=E, k=k, I=I, Is=0))
+    mb.moe_block_fp8(dev(X), dev(Wr), k, mb.Fp8Experts(W13.view(F8), s13, W2.view(F8), s2), out, ws, bias=dev(bias), topk_ids=ids)
+    assert np.array_equal(host(ids), np.tile([5, E - 1], (B, 1)))
+    full = np.tile(bias.astype(np.float64), (B, 1))
+    want, _, _ = ref.moe(widen(X), widen(Wr), k, lambda e: ref.VALUES[W13[e].cpu().numpy()] * 2.0 ** -14,
+                         lambda e: ref.VALUES[W2[e].cpu().numpy()] * 2.0 ** -10, full)
+    check_block_output(host(out), want)
+
+
+@pytest.mark.parametrize("variant", ["gemv", "splitk", "mfma"])
+def test_block_with_a_forced_router(variant):
+    """A forced shape is the router's: same choices, an output within the bars; refused where it does not reach."""
+    c = Moe(2, 256, 32, 4, 64, 64, "plain", seed=11)
+    out, ids, w = c.outputs()
+    prev = mb.set_variant(variant)
+    try:
+        c.call(out.t, ids.t, w.t)
+        big = Moe(20, 256, 32, 4, 64, 64, "plain", seed=11)
+        o = torch.empty((20, 256), dtype=torch.bfloat16, device="cuda")
+        if variant == "mfma":
+            big.call(o)
+        else:
+            with pytest.raises(mb.MoeError) as e:
+                big.call(o)
+            assert e.value.status == mb.EUNSUPPORTED
+    finally:
+        mb.set_variant(prev)
+    want, want_ids, _ = c.reference()
+    assert np.array_equal(host(ids.t), want_ids)
+    check_block_output(host(out.t), want)
+
+
+@pytest.mark.parametrize("B", [2, 7, 12, 40])
+def test_block_a_token_that_is_not_finite_stays_alone(B):
+    c = Moe(B, 256, 32, 4, 64, 64, "plain", seed=12)
+    a, b = torch.empty((B, 256), dtype=torch.bfloat16, device="cuda"), torch.empty((B, 256), dtype=torch.bfloat16, device="cuda")
+    c.call(a)
+    X = c.X.clone()
+    X[1, 7] = float("nan")
+    c.call(b, X=X)
+    rows = [t for t in range(B) if t != 1]
+    assert torch.equal(a[rows].view(torch.int16), b[rows].view(torch.int16))
+    assert mb.workspace_status(c.ws) == 0
+
+
+def test_one_workspace_serves_every_op_in_turn():
+    """Dense with K slices, blocks of 8-bit and of bf16 weights, large and small, over one workspace: each call leaves
+    its counters as it found them."""
+    g = Dense(40, 300, 4096, "bf16", seed=13)
+    assert g.ws_buf is not None
+    blocks = [Moe(B, 512, 32, 4, 64, 64, "plain", seed=13) for B in (1, 2, 8, 40)]
+    W13 = (torch.randn((32, 128, 512), device="cuda") * 0.04).to(torch.bfloat16)
+    W2 = (torch.randn((32, 512, 64), device="cuda") * 0.1).to(torch.bfloat16)
+    ws = mb.workspace(max([g.ws_buf.numel()] + [c.ws.numel() for c in blocks] + [
+        mb.workspace_bytes(mb.OP_BLOCK, mb.DT_BF16, B=B, d=512, E=32, k=4, I=64, Is=0) for B in (1, 40)]))
+    want = []
+    for rep in range(3):
+        got = []
+        for c in blocks:
+            o = torch.empty((c.B, 512), dtype=torch.bfloat16, device="cuda")
+            c.call(o, ws=ws)
+            got.append(o)
+            y = torch.empty((40, 300), dtype=torch.float32, device="cuda")
+            mb.skinny_gemm_fp8(g.args[0], g.weight, y, ws=ws)
+            got.append(y)
+            z = torch.empty((c.B, 512), dtype=torch.bfloat16, device="cuda")
+            mb.moe_block(c.X, c.gWr, 4, W13, W2, z, ws)
+            got.append(z)
+        torch.cuda.synchronize()
+        want = want or got
+        for p, q in zip(want, got):
+            assert torch.equal(p, q)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with a workspace of its own: the bits of the calls one after the other."""
+    g = Dense(64, 6400, 4096, "e4m3", seed=14)
+    c = Moe(8, 1024, 64, 8, 128, 128, "gumbel", seed=14)
+    y0, o0 = torch.empty((64, 6400), device="cuda"), torch.empty((8, 1024), dtype=torch.bfloat16, device="cuda")
+    g.call(y0)
+    c.call(o0)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    y, o = [torch.empty_like(y0) for _ in range(20)], [torch.empty_like(o0) for _ in range(20)]
+    for i in range(20):
+        g.call(y[i], stream=s)
+        c.call(o[i], stream=t)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y0, v) for v in y) and all(torch.equal(o0, v) for v in o)
+
+
+def test_shared_kernel_replays():
+    """The dense product with K slices in a graph, replayed between eager calls on the same workspace."""
+    g = Dense(40, 300, 4096, "e4m3", seed=15)
+    h = Dense(64, 300, 4096, "bf16", seed=15)
+    ws = mb.workspace(max(g.ws_buf.numel(), h.ws_buf.numel()))
+    g.ws_buf = h.ws_buf = ws
+    R = dev(g.R)
+    Y, Z = torch.empty((40, 300), dtype=torch.bfloat16, device="cuda"), torch.empty((64, 300), device="cuda")
+    g.call(Y, R)
+    h.call(Z)
+    torch.cuda.synchronize()
+    y, z = Y.clone(), Z.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        g.call(Y, R)
+    for rep in range(4):
+        Y.zero_()
+        graph.replay()
+        h.call(Z)
+        torch.cuda.synchronize()
+        assert torch.equal(Y, y) and torch.equal(Z, z), rep
