@@ -178,7 +178,8 @@ int moe_plan_words(int B, int k, int E);
  *   MOE_OP_BLOCK:       dtype, B, d, E, k, I, Is
  *   MOE_OP_ROUTE_LATENT: dtype, B, d, E, k, and N = L (the latent rows)
  *   MOE_OP_SKINNY_GEMM_FP8: dtype (of X), B, N, K
- *   MOE_OP_BLOCK_FP8:   dtype, B, d, E, k, I, Is */
+ *   MOE_OP_BLOCK_FP8:   dtype, B, d, E, k, I, Is
+ * The last two are 0 for sizes past their call's scope. */
 size_t moe_workspace_bytes(int op, int dtype, int B, int d, int E, int k, int I, int Is, int N,
                            int K);
 

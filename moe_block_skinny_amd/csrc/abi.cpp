@@ -303,10 +303,14 @@ BlockWs block_ws(int bf16, int B, int d, int E, int k, int I, int Is) {
   return b;
 }
 
+constexpr int kMaxK8 = 65536;        // columns of an 8-bit product: byte offsets within 64 rows stay below 2^31
+constexpr int kMaxN8 = 1 << 24;
+
 // Dense product over 8-bit weights: after the header, the K slices' sums.
 // The row groups' arrival counters are the header's words from 32 on: with
 // more than one slice there are at most 128 of them.
 size_t gemm_fp8_ws(int B, int N, int K) {
+  if (B > kMaxB || N > kMaxN8 || K > kMaxK8) return 0;   // refused by the call; the plan's sums would pass 31 bits
   const size_t part = gemm_fp8_plan(B, N, K).part_bytes;
   return part ? up(kHeaderBytes + part) : 0;
 }
@@ -575,7 +579,8 @@ size_t moe_workspace_bytes(int op, int dtype, int B, int d, int E, int k, int I,
       if (N <= 0 || K <= 0) return 0;
       return gemm_fp8_ws(B, N, K);
     case MOE_OP_BLOCK_FP8:
-      if (E <= 0 || d <= 0 || k <= 0) return 0;
+      if (E <= 0 || d <= 0 || k <= 0 || I < 0 || Is < 0) return 0;
+      if (B > kMaxB || E > kMaxE || k > kMaxK || d > kMaxK8 || I > kMaxI || Is > kMaxI) return 0;
       return block_fp8_ws(B, d, E, k, I, Is).total;
   }
   return 0;
@@ -1056,9 +1061,6 @@ moe_status_t moe_block_noalloc(int dtype, int B, int d, int E, int k, int I, int
 // ---- 8-bit weights ------------------------------------------------------------
 
 namespace {
-
-constexpr int kMaxK8 = 65536;        // columns of an 8-bit product: byte offsets within 64 rows stay below 2^31
-constexpr int kMaxN8 = 1 << 24;
 
 moe_status_t block_fp8_run(int B, int d, int E, int k, int I, int Is, const void* X, const void* Wr, const float* bias,
                            int bias_ld, const moe_fp8_experts_t& W, void* out, int32_t* topk_ids, float* topk_w,

@@ -2,6 +2,9 @@
 the documented status before any HIP call (fake device pointers, only in calls
 that must fail), and by the binding before any pointer reaches the library."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -174,3 +177,31 @@ def test_block_rejects():
                       (dict(topk_ids=z(2, 2, dtype=torch.int64)), TypeError), (dict(topk_w=z(2, 3, dtype=f32)), ValueError)):
         with pytest.raises(exc):
             mb.moe_block_fp8(**{**ok, **over})
+
+
+# ---- sizes past the scope --------------------------------------------------------
+
+
+QUERIES = r"""
+from moe_block_skinny_amd import binding as mb
+top = 2 ** 31 - 1
+for B in (1, 17, 64, 65, 1 << 20, 1 << 24, top):
+    for N in (1, 6400, 1 << 24, top):
+        for K in (16, 4096, 65536, top):
+            got = mb.workspace_bytes(mb.OP_SKINNY_GEMM_FP8, mb.DT_BF16, B=B, N=N, K=K)
+            if B > 64 or N > 1 << 24 or K > 65536:
+                assert got == 0, (B, N, K, got)
+ok = dict(B=64, d=256, E=16, k=4, I=64, Is=32)
+assert mb.workspace_bytes(mb.OP_BLOCK_FP8, mb.DT_BF16, **ok) > 0
+for name, bad in (("B", (65, 1 << 24, top)), ("d", (65568, top)), ("E", (513, top)), ("k", (17, top)),
+                  ("I", (-32, 257, top)), ("Is", (-32, 257, top))):
+    for v in bad:
+        assert mb.workspace_bytes(mb.OP_BLOCK_FP8, mb.DT_BF16, **{**ok, name: v}) == 0, (name, v)
+"""
+
+
+def test_workspace_queries_past_the_scope():
+    # in a process of its own: a query that divided by a size that had wrapped to zero ended the process
+    r = subprocess.run([sys.executable, "-c", QUERIES], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=110)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
