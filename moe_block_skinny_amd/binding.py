@@ -460,6 +460,15 @@ def _groups(n):
     return (n + FP8_BLOCK - 1) // FP8_BLOCK
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _sizes(name, *sizes):
+    """Sizes for a C int, which would keep the low bits of longer ones."""
+    if max(sizes) > _INT_MAX:
+        raise ValueError("%s: sizes %s past %d" % (name, sizes, _INT_MAX))
+
+
 def _on(name, t, shape, dtype, index):
     """The checks of _Args.arr and on_gpu for one tensor of a call on GPU `index` (-1: host memory, refused
     later); its address.  One condition for what passes: the checks are most of a small call's host time."""
@@ -510,6 +519,7 @@ class Fp8Weight:
 
     def __init__(self, codes, scale):
         self.N, self.K = _shape("codes", codes, 2)
+        _sizes("codes", self.N, self.K)
         self.index = codes.get_device()
         a = _Args()
         a.arr("codes", codes, (self.N, self.K), torch.float8_e4m3fn)
@@ -531,6 +541,7 @@ class Fp8Experts:
 
     def __init__(self, W13, s13, W2, s2, Ws13=None, ss13=None, Ws2=None, ss2=None):
         self.E, two_i, self.d = _shape("W13", W13, 3)
+        _sizes("W13", self.E, two_i, self.d)
         if two_i % 2:
             raise ValueError("W13: [E][2I][d] expected, got %s" % (tuple(W13.shape),))
         E, d, I = self.E, self.d, two_i // 2
@@ -546,6 +557,7 @@ class Fp8Experts:
             if not all(given):
                 raise ValueError("Ws13, ss13, Ws2 and ss2 come together (all or none)")
             two_s, _ = _shape("Ws13", Ws13, 2)
+            _sizes("Ws13", two_s)
             if two_s % 2:
                 raise ValueError("Ws13: [2Is][d] expected, got %s" % (tuple(Ws13.shape),))
             Is = self.Is = two_s // 2
@@ -571,6 +583,7 @@ def moe_quantize_fp8(X, Q, scale, layout, stream=None):
     shape = X.shape
     if len(shape) not in (2, 3):
         raise ValueError("X: [rows][cols] or [n][rows][cols] expected, got shape %s" % (tuple(shape),))
+    _sizes("X", *shape)
     lead, (rows, cols) = shape[:-2], shape[-2:]
     dt = _dt(X)
     x = _on("X", X, shape, X.dtype, index)
@@ -614,7 +627,10 @@ def _rows(X):
         raise TypeError("X: a torch.Tensor expected, got %s" % type(X).__name__)
     if X.dim() != 2:
         raise ValueError("X: 2 dimensions expected, got shape %s" % (tuple(X.shape),))
-    return X.shape[0]
+    B = X.shape[0]
+    if B > _INT_MAX:
+        _sizes("X", B)
+    return B
 
 
 def moe_block_fp8(X, Wr, k, experts, out, ws, bias=None, bias_ld=0, topk_ids=None, topk_w=None, stream=None):
@@ -623,6 +639,8 @@ def moe_block_fp8(X, Wr, k, experts, out, ws, bias=None, bias_ld=0, topk_ids=Non
         raise TypeError("experts: an Fp8Experts expected, got %s" % type(experts).__name__)
     index, E, d, I, Is = experts.index, experts.E, experts.d, experts.I, experts.Is
     B = _rows(X)
+    if k > _INT_MAX:
+        _sizes("k", k)
     x = _on("X", X, (B, d), torch.bfloat16, index)
     wr = _on("Wr", Wr, (E, d), torch.bfloat16, index)
     b = None

@@ -205,3 +205,25 @@ def test_workspace_queries_past_the_scope():
     r = subprocess.run([sys.executable, "-c", QUERIES], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                        capture_output=True, text=True, timeout=110)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+def test_binding_refuses_sizes_past_31_bits():
+    # a C int keeps their low bits: [2^32 + 8][16] would be taken for 8 rows
+    def big(*shape, dtype=bf):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    n = 2 ** 32 + 8
+    with pytest.raises(ValueError, match="2147483647"):
+        mb.moe_quantize_fp8(big(n, 16), big(n, 16, dtype=f8), big(n, 1, dtype=f32), "rows")
+    with pytest.raises(ValueError, match="2147483647"):
+        mb.moe_quantize_fp8(big(n, 2, 16), big(n, 2, 16, dtype=f8), big(n, 2, 1, dtype=f32), "rows")
+    with pytest.raises(ValueError, match="2147483647"):
+        mb.skinny_gemm_fp8(big(n, 256), weight(), big(n, 64))
+    with pytest.raises(ValueError, match="2147483647"):
+        mb.Fp8Weight(big(n, 16, dtype=f8), big((n + 127) // 128, 1, dtype=f32))
+    with pytest.raises(ValueError, match="2147483647"):
+        mb.Fp8Experts(big(n, 64, 32, dtype=f8), big(n, 2, 1, dtype=f32), big(n, 32, 32, dtype=f8), big(n, 1, 1, dtype=f32))
+    e = mb.Fp8Experts.__new__(mb.Fp8Experts)
+    e.E, e.d, e.I, e.Is, e.index, e._ref = 8, 64, 32, 0, -1, None
+    with pytest.raises(ValueError, match="2147483647"):
+        mb.moe_block_fp8(z(2, 64), z(8, 64), n, e, z(2, 64), z(1024, dtype=torch.uint8))
