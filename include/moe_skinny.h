@@ -457,7 +457,8 @@ moe_status_t moe_quantize_fp8(int layout, int dtype, int n, int rows, int cols, 
  *   each 128-column block summed in fp32, then added to the fp32 sum of the
  *   row by its scale.
  *   X [B][K]: bf16 (x_scale NULL), or e4m3 with x_scale [B][ceil(K / 128)],
- *   which then multiplies too.  W [N][K] e4m3, w_scale
+ *   which then multiplies too (the two scales first, in fp32: their product
+ *   must be a finite one).  W [N][K] e4m3, w_scale
  *   [ceil(N / 128)][ceil(K / 128)], R [B][N] bf16, Y [B][N] bf16 or fp32.
  *   Y may be R itself (bf16) but must not otherwise overlap an input.
  *   1 <= B <= 64, K a multiple of 16 up to 65536, N up to 2^24.  Workspace:

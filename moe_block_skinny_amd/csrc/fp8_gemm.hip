@@ -87,7 +87,7 @@ constexpr int kQuantThreads = 256;
 
 template <typename T>
 __global__ __launch_bounds__(kQuantThreads) void quantize_rows_kernel(QuantizeLaunch a) {
-  const uint32_t KB = (uint32_t)(a.cols + kQBlock - 1) / kQBlock;
+  const uint32_t KB = ((uint32_t)a.cols + kQBlock - 1) / kQBlock;   // cols may end at 2^31 - 16
   const uint32_t groups = (uint32_t)a.rows * KB;   // all matrices' rows, < 2^31
   const uint32_t stride = gridDim.x * (kQuantThreads / 8);
   const int c = threadIdx.x & 7;
@@ -117,7 +117,7 @@ template <typename T>
 __global__ __launch_bounds__(kQuantThreads) void quantize_blocks_kernel(QuantizeLaunch a) {
   constexpr int R = 4, kRows = kQuantThreads / 8;
   __shared__ float s_max[kQuantThreads / 64];
-  const uint32_t KB = (uint32_t)(a.cols + kQBlock - 1) / kQBlock, RB = (uint32_t)(a.rows + kQBlock - 1) / kQBlock;
+  const uint32_t KB = ((uint32_t)a.cols + kQBlock - 1) / kQBlock, RB = ((uint32_t)a.rows + kQBlock - 1) / kQBlock;
   const uint32_t bc = blockIdx.x % KB, t = blockIdx.x / KB, br = t % RB, n = t / RB;
   const int col = (int)bc * kQBlock + 16 * (threadIdx.x & 7);
   const int row0 = (int)br * kQBlock + (threadIdx.x >> 3);

@@ -469,6 +469,21 @@ def test_quantize_past_4_gib(layout):
     assert not Q[: rows - 129].view(torch.uint8).any() and bool((S[: S.shape[0] - s.shape[1]] == 1).all())
 
 
+def test_quantize_longest_row():
+    # the last group, 112 columns, ends at column 2^31 - 16
+    cols, t = 2 ** 31 - 16, 240
+    X = torch.zeros((1, cols), dtype=torch.bfloat16, device="cuda")
+    th = bf16(hard_values(rng(10), 1, 1, t))[0]
+    X[:, cols - t:] = dev(th)
+    Q = torch.empty((1, cols), dtype=F8, device="cuda")
+    S = torch.empty((1, ref.blocks(cols)), device="cuda")
+    mb.moe_quantize_fp8(X, Q, S, "rows")
+    q, s = ref.quantize(widen(th)[None], "rows")
+    assert np.array_equal(codes_of(Q[:, cols - t:]), q[0])
+    assert np.array_equal(host(S[:, -2:]), s[0])
+    assert not Q[:, : cols - t].view(torch.uint8).any() and bool((S[:, :-2] == 1).all())
+
+
 @pytest.mark.parametrize("B", [3, 20])
 def test_block_experts_past_4_gib_and_widest_hidden_size(B):
     """d = 65536, and W13 of more than 2^32 bytes with the last expert chosen by every token."""
