@@ -21,9 +21,9 @@
 // through LDS -- a buffer of the wave's own, no barrier -- and is read back as
 // the operand: lane l = R + 16 g holds columns 32 g .. 32 g + 31 of row R.
 // Activations of more than 8 tokens take the same way.  Within a row of the
-// buffer the 16-byte pieces are permuted by the row's low bits (exclusive or),
-// so that eight lanes reading one piece of eight rows meet eight different
-// bank groups.
+// buffer the 16-byte pieces are permuted by exclusive or with a number of the
+// row (swizzle128, swizzle256), so that the lanes of a read that are served
+// together meet different banks.
 #pragma once
 
 #include "common.hpp"
@@ -128,29 +128,43 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t w0, uint32_t w1) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// LDS serves a 128-bit read 16 lanes (all 64 banks) at a time, and those are
+// lanes 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31, then the same 32
+// higher (measured: two lanes of one group on the same banks take longer).  As
+// operand reads that is rows 0-3 and 12-15 of one lane group with rows 4-11 of
+// its neighbour, whose pieces differ in bit 1 (128-byte rows, two to a round
+// of the banks) or bit 2 (256-byte rows): the numbers of the former rows have
+// to be a set that this bit maps onto itself.  Permuted by the row's low bits
+// alone a read took 8.2 cycles, so 5.0; 1536 x 7168, 64 tokens: 13.7 -> 13.5 us.
+__device__ __forceinline__ int swizzle128(int row) {
+  const int r = row >> 1;
+  return r ^ ((r & 2) << 1);   // of row + 8: the same with bit 2 flipped
+}
+__device__ __forceinline__ int swizzle256(int row) { return row ^ ((row & 4) << 1); }
+
 // 16 rows x 128 bytes through LDS: rows lane / 8 (a) and 8 + lane / 8 (b),
 // piece lane % 8, in; row lane % 16, pieces 2 g and 2 g + 1 out.  One wave's
 // LDS accesses are served in order, so no wait stands between them.
 __device__ __forceinline__ void rows128_store(int lane, char* lds, u32x4 a, u32x4 b) {
-  u32x4* p = reinterpret_cast<u32x4*>(lds) + ((lane & ~7) | ((lane & 7) ^ (lane >> 3)));
-  p[0] = a;
-  p[64] = b;
+  const int i = (lane & ~7) | ((lane & 7) ^ swizzle128(lane >> 3));
+  reinterpret_cast<u32x4*>(lds)[i] = a;
+  reinterpret_cast<u32x4*>(lds)[64 + (i ^ 4)] = b;
 }
 __device__ __forceinline__ void rows128_load(int lane, const char* lds, u32x4& lo, u32x4& hi) {
   const int R = lane & 15, g = lane >> 4;
   const u32x4* p = reinterpret_cast<const u32x4*>(lds) + R * 8;
-  lo = p[(2 * g) ^ (R & 7)];
-  hi = p[(2 * g + 1) ^ (R & 7)];
+  lo = p[(2 * g) ^ swizzle128(R)];
+  hi = p[(2 * g + 1) ^ swizzle128(R)];
 }
 // 16 rows x 256 bytes: row 4 i + lane / 16, piece lane % 16, in; row
 // lane % 16, piece 4 g + j out.
 __device__ __forceinline__ void rows256_store(int lane, char* lds, int i, u32x4 v) {
   const int t = 4 * i + (lane >> 4);
-  reinterpret_cast<u32x4*>(lds)[t * 16 + ((lane & 15) ^ t)] = v;
+  reinterpret_cast<u32x4*>(lds)[t * 16 + ((lane & 15) ^ swizzle256(t))] = v;
 }
 __device__ __forceinline__ u32x4 rows256_load(int lane, const char* lds, int j) {
   const int t = lane & 15, g = lane >> 4;
-  return reinterpret_cast<const u32x4*>(lds)[t * 16 + ((4 * g + j) ^ t)];
+  return reinterpret_cast<const u32x4*>(lds)[t * 16 + ((4 * g + j) ^ swizzle256(t))];
 }
 
 // Registers of one K block of a wave.
@@ -426,11 +440,11 @@ __device__ __forceinline__ void shared_product(const SharedSrc<RT, NT, E8>& s, i
       if constexpr (E8) {
         if (NT % 2 == 0 || t < 16 * NT) {
           const u32x4 v = k0 + 16 * (ht & 7) < K ? xv[u][q] : zero;
-          row[(2 * (ht & 7)) ^ (t & 15)] = __builtin_bit_cast(u32x4, widen8(v[0], v[1]));
-          row[(2 * (ht & 7) + 1) ^ (t & 15)] = __builtin_bit_cast(u32x4, widen8(v[2], v[3]));
+          row[(2 * (ht & 7)) ^ swizzle256(t & 15)] = __builtin_bit_cast(u32x4, widen8(v[0], v[1]));
+          row[(2 * (ht & 7) + 1) ^ swizzle256(t & 15)] = __builtin_bit_cast(u32x4, widen8(v[2], v[3]));
         }
       } else {
-        row[(ht & 15) ^ (t & 15)] = k0 + 8 * (ht & 15) < K ? xv[u][q] : zero;
+        row[(ht & 15) ^ swizzle256(t & 15)] = k0 + 8 * (ht & 15) < K ? xv[u][q] : zero;
       }
     }
   };
@@ -462,7 +476,7 @@ __device__ __forceinline__ void shared_product(const SharedSrc<RT, NT, E8>& s, i
       for (int rt = 0; rt < RT; ++rt) d[rt] = fzero;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf16x8 xj = __builtin_bit_cast(bf16x8, row[(4 * g + j) ^ c16]);
+        const bf16x8 xj = __builtin_bit_cast(bf16x8, row[(4 * g + j) ^ swizzle256(c16)]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) d[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[rt][j], xj, d[rt], 0, 0, 0);
       }
