@@ -510,9 +510,11 @@ __device__ __forceinline__ void shared_product(const SharedSrc<RT, NT, E8>& s, i
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (u + 1 < U) stage(i + u + 1, u + 1);
-    if (i + u < n) compute(i + u, u);
-    lds_barrier();
+    if (i + u < iters) {   // uniform; 7 blocks of a half are not run as 8 (64 tokens, 7168 x 7168: 0.2 us)
+      if (u + 1 < U && i + u + 1 < iters) stage(i + u + 1, u + 1);
+      if (i + u < n) compute(i + u, u);
+      lds_barrier();
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
 }
