@@ -20,10 +20,11 @@
 // different rows, as the matrix operand wants them.  So what is loaded goes
 // through LDS -- a buffer of the wave's own, no barrier -- and is read back as
 // the operand: lane l = R + 16 g holds columns 32 g .. 32 g + 31 of row R.
-// Activations of more than 8 tokens take the same way.  Within a row of the
-// buffer the 16-byte pieces are permuted by exclusive or with a number of the
-// row (swizzle128, swizzle256), so that the lanes of a read that are served
-// together meet different banks.
+// Activations of more than 8 tokens, and of 5 to 8 over a long row, take the
+// same way.  Within a row of the buffer the 16-byte pieces are permuted by
+// exclusive or with a number of the row (swizzle128, swizzle256,
+// swizzle_packed), so that the lanes of a read that are served together meet
+// different banks.
 #pragma once
 
 #include "common.hpp"
@@ -39,6 +40,11 @@ constexpr int kQBlock = 128;   // columns (and weight rows) that share a scale
 //         the columns that hold piece j, the others as zeros, so the four
 //         columns of a token add up to its sum.
 //   XP8:  bf16, up to 8 tokens, two loads: column 2 t + (j & 1).
+//   XP8L: the same columns through LDS: two loads of 4 tokens x 256 bytes, not
+//         of 32 bytes of a token to a lane pair.  For rows of several steps:
+//         57344 x 7168, 8 tokens, 80 us with XP8, 75.5 with XP8L; 7168 x 2048,
+//         6 tokens, all requested at once, 5.7 and 5.8; gate/up of 64 tokens
+//         2 % more.
 //   XB:   bf16, NT tiles of 16 tokens, through LDS: four loads of 4 tokens x
 //         256 bytes per tile.
 //   X8P:  e4m3, up to 8 tokens, one load: column 2 t + i holds the lane
@@ -47,7 +53,7 @@ constexpr int kQBlock = 128;   // columns (and weight rows) that share a scale
 //         128 bytes per tile.
 // A token packed in 4 columns costs a quarter of the registers that a column
 // of its own would, which is what lets a wave request all its blocks at once.
-enum XKind { XP4 = 0, XP8 = 1, XB = 2, X8P = 3, X8 = 4 };
+enum XKind { XP4 = 0, XP8 = 1, XB = 2, X8P = 3, X8 = 4, XP8L = 5 };
 
 constexpr bool x_e4m3(int xk) { return xk == X8P || xk == X8; }
 
@@ -56,6 +62,7 @@ constexpr bool x_e4m3(int xk) { return xk == X8P || xk == X8; }
 template <int XK> struct XTraits;
 template <> struct XTraits<XP4> { static constexpr int kLoads = 1, kTokens = 4, kCols = 4, kLds = 0; };
 template <> struct XTraits<XP8> { static constexpr int kLoads = 2, kTokens = 8, kCols = 2, kLds = 0; };
+template <> struct XTraits<XP8L> { static constexpr int kLoads = 2, kTokens = 8, kCols = 2, kLds = 2048; };
 template <> struct XTraits<XB> { static constexpr int kLoads = 4, kTokens = 16, kCols = 1, kLds = 4096; };
 template <> struct XTraits<X8P> { static constexpr int kLoads = 1, kTokens = 8, kCols = 2, kLds = 0; };
 template <> struct XTraits<X8> { static constexpr int kLoads = 2, kTokens = 16, kCols = 1, kLds = 2048; };
@@ -76,13 +83,13 @@ __device__ __forceinline__ int x_column_token(int lane) {
 // Token whose values this lane requests with load i.
 template <int XK>
 __device__ __forceinline__ int x_load_token(int lane, int i) {
-  if constexpr (XK == XB) return 4 * i + (lane >> 4);
+  if constexpr (XK == XB || XK == XP8L) return 4 * i + (lane >> 4);
   else if constexpr (XK == X8) return 8 * i + (lane >> 3);
   else return x_column_token<XK>(lane);
 }
 // Distinct tokens among a lane's loads of a tile.
 template <int XK>
-constexpr int x_rows() { return (XK == XB || XK == X8) ? XTraits<XK>::kLoads : 1; }
+constexpr int x_rows() { return XTraits<XK>::kLds ? XTraits<XK>::kLoads : 1; }
 
 // Loads go through buffer descriptors: an offset past their end (kNoLoad and
 // more) reads zeros and asks nothing of memory, which is how rows, tokens and
@@ -141,6 +148,7 @@ __device__ __forceinline__ int swizzle128(int row) {
   return r ^ ((r & 2) << 1);   // of row + 8: the same with bit 2 flipped
 }
 __device__ __forceinline__ int swizzle256(int row) { return row ^ ((row & 4) << 1); }
+__device__ __forceinline__ int swizzle_packed(int t) { return 2 * (t ^ ((t & 2) << 1)); }   // of 8 rows, pairs of pieces
 
 // 16 rows x 128 bytes through LDS: rows lane / 8 (a) and 8 + lane / 8 (b),
 // piece lane % 8, in; row lane % 16, pieces 2 g and 2 g + 1 out.  One wave's
@@ -167,6 +175,17 @@ __device__ __forceinline__ u32x4 rows256_load(int lane, const char* lds, int j) 
   return reinterpret_cast<const u32x4*>(lds)[t * 16 + ((4 * g + j) ^ swizzle256(t))];
 }
 
+// 8 rows x 256 bytes: row 4 i + lane / 16, piece lane % 16, in; row
+// (lane % 16) / 2, piece 4 g + 2 i + lane % 2 out.
+__device__ __forceinline__ void packed256_store(int lane, char* lds, int i, u32x4 v) {
+  const int t = 4 * i + (lane >> 4);
+  reinterpret_cast<u32x4*>(lds)[t * 16 + ((lane & 15) ^ swizzle_packed(t))] = v;
+}
+__device__ __forceinline__ u32x4 packed256_load(int lane, const char* lds, int i) {
+  const int t = (lane & 15) >> 1, g = lane >> 4;
+  return reinterpret_cast<const u32x4*>(lds)[t * 16 + ((4 * g + 2 * i + (lane & 1)) ^ swizzle_packed(t))];
+}
+
 // Registers of one K block of a wave.
 template <int XK, int RT, int NT>
 struct Fp8Block {
@@ -187,7 +206,7 @@ __device__ __forceinline__ void fp8_load(const Fp8Src<XK, RT, NT>& s, int kb, Fp
       uint32_t c = k0;   // column of the lane's 16 bytes
       if constexpr (XK == XP4) c += 32 * g + 8 * (lane & 3);
       else if constexpr (XK == XP8) c += 32 * g + 16 * i + 8 * (lane & 1);
-      else if constexpr (XK == XB) c += 8 * (lane & 15);
+      else if constexpr (XK == XP8L || XK == XB) c += 8 * (lane & 15);
       else if constexpr (XK == X8P) c += 32 * g + 16 * (lane & 1);
       else c += 16 * (lane & 7);
       const uint32_t o = s.xo[nt][x_rows<XK>() > 1 ? i : 0] + (x_e4m3(XK) ? c : 2 * c);
@@ -226,6 +245,11 @@ __device__ __forceinline__ void fp8_block(int lane, const Fp8Block<XK, RT, NT>& 
       for (int i = 0; i < 4; ++i) rows256_store(lane, xl, i, r.x[nt][i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[nt][j] = rows256_load(lane, xl, j);
+    } else if constexpr (XK == XP8L) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) packed256_store(lane, xl, i, r.x[nt][i]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) h[nt][i] = packed256_load(lane, xl, i);
     } else if constexpr (XK == X8) {
       rows128_store(lane, xl, r.x[nt][0], r.x[nt][1]);
       rows128_load(lane, xl, h[nt][0], h[nt][1]);
@@ -242,7 +266,7 @@ __device__ __forceinline__ void fp8_block(int lane, const Fp8Block<XK, RT, NT>& 
       return widen8(mine ? w0 : 0u, mine ? w1 : 0u);
     } else if constexpr (XK == XP4) {
       return __builtin_bit_cast(bf16x8, (lane & 3) == j ? h[nt][0] : zero);
-    } else if constexpr (XK == XP8) {
+    } else if constexpr (XK == XP8 || XK == XP8L) {
       return __builtin_bit_cast(bf16x8, (lane & 1) == (j & 1) ? h[nt][j >> 1] : zero);
     } else {
       return __builtin_bit_cast(bf16x8, h[nt][j]);

@@ -482,7 +482,8 @@ hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* sha
     }
   } else {
     if (a.M <= 4) go<XP4, 1, 1, 2, 8>(a, st, shape);
-    else if (a.M <= 8) go<XP8, 1, 1, 2, 8>(a, st, shape);
+    else if (a.M <= 8 && a.K <= 8 * 2 * kQBlock) go<XP8, 1, 1, 2, 8>(a, st, shape);   // one step of 8 waves x 2 blocks
+    else if (a.M <= 8) go<XP8L, 1, 1, 2, 8>(a, st, shape);
     else if (nt <= 1) go<XB, 1, 1, 2, 4>(a, st, shape);
     else if (a.N < kMinNForTwoTiles) {
       if (nt == 2) go<XB, 1, 2, 2, 8>(a, st, shape);

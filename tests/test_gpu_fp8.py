@@ -157,6 +157,18 @@ def test_gemm_against_64_bits(B, N, K, xt):
         Y.check()
 
 
+@pytest.mark.parametrize("B,N,K", [(5, 33, 2048), (6, 100, 2064), (8, 1001, 2176), (8, 40, 4112), (7, 257, 8208), (33, 300, 7168)])
+def test_gemm_rows_of_several_steps(B, N, K):
+    # 5 to 8 tokens on both sides of the row length that changes their layout; K slices of an odd number of blocks
+    c = Dense(B, N, K, "bf16")
+    for out, residual in (("f32", False), ("bf16", True)):
+        Y = Guarded((B, N), torch.float32 if out == "f32" else torch.bfloat16)
+        c.call(Y.t, dev(c.R) if residual else None)
+        torch.cuda.synchronize()
+        c.check(host(Y.t), residual, out)
+        Y.check()
+
+
 @pytest.mark.parametrize("B,N,K,xt", [(3, 130, 400, "bf16"), (20, 130, 400, "bf16"), (20, 130, 400, "e4m3")])
 def test_gemm_small_integers_are_exact(B, N, K, xt):
     """Codes of small integers, scales of powers of two: every sum is exact in fp32, whatever its order."""
