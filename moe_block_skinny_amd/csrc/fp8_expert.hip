@@ -518,13 +518,35 @@ __global__ __launch_bounds__(DownWaves<KBM>::kMax * 64) void expert_down_combine
     d.products(v, sc, h);
   }
   __syncthreads();
-  const int has_shared = x.Ws13 ? 1 : 0;
-  for (int i = threadIdx.x; i < x.B * rows; i += blockDim.x) {
-    const int t = i / rows, r = i - t * rows;
+  // four rows a thread (rows, r0 and d are multiples of 4), in combine_one's
+  // order; four slots' outputs requested at a time
+  const int quads = rows / 4;
+  for (int i = threadIdx.x; i < x.B * quads; i += blockDim.x) {
+    const int t = i / quads, r = 4 * (i - t * quads);
     if (r0 + r >= x.d) continue;
-    const float v = combine_one(s_tw + t * x.k, x.k, has_shared,
-                                [&](int j) { return s_y[(size_t)(j < x.k ? t * x.k + j : x.B * x.k + t) * rows + r]; });
-    reinterpret_cast<bf16_t*>(x.out)[(size_t)t * x.d + r0 + r] = f32_to_bf16(v);
+    const float* w = s_tw + t * x.k;
+    auto y_of = [&](int slot) { return *reinterpret_cast<const f32x4*>(s_y + (size_t)slot * rows + r); };
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < x.k; j0 += 4) {
+      f32x4 y[4];
+      float wj[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = j0 + q < x.k ? j0 + q : x.k - 1;
+        y[q] = y_of(t * x.k + j);
+        wj[q] = w[j];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j0 + q < x.k) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(wj[q], y[q][e], v[e]);
+        }
+    }
+    if (x.Ws13) v += y_of(x.B * x.k + t);
+    const u32x2 o = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                     (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+    *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(x.out) + (size_t)t * x.d + r0 + r) = o;
   }
 }
 
