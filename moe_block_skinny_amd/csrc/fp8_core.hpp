@@ -42,9 +42,9 @@ constexpr int kQBlock = 128;   // columns (and weight rows) that share a scale
 //   XP8:  bf16, up to 8 tokens, two loads: column 2 t + (j & 1).
 //   XP8L: the same columns through LDS: two loads of 4 tokens x 256 bytes, not
 //         of 32 bytes of a token to a lane pair.  For rows of several steps:
-//         57344 x 7168, 8 tokens, 80 us with XP8, 75.5 with XP8L; 7168 x 2048,
-//         6 tokens, all requested at once, 5.7 and 5.8; gate/up of 64 tokens
-//         2 % more.
+//         57344 x 7168, 8 tokens, 80 us with XP8, 75.5 with XP8L (2 blocks in
+//         flight); 7168 x 2048, 6 tokens, all requested at once, 5.7 and 5.8;
+//         gate/up of 64 tokens 2 % more.
 //   XB:   bf16, NT tiles of 16 tokens, through LDS: four loads of 4 tokens x
 //         256 bytes per tile.
 //   X8P:  e4m3, up to 8 tokens, one load: column 2 t + i holds the lane

@@ -79,7 +79,7 @@ __device__ __forceinline__ void fp8_token(const Fp8ExpertLaunch& a, const int32_
 //   times as long (37 against 130 bytes/ns), and h crosses once per
 //   workgroup.  An entry of up to kRowTokens tokens keeps plain rows in its
 //   tile all the same: a tile's steps would bring in a cache line for every
-//   16 bytes of a lone token.
+//   16 bytes of a lone token (49.8 us for the batch-32 block, 49.9 without).
 constexpr int kRowTokens = 4;
 __device__ __forceinline__ uint32_t h_tile(const Fp8ExpertLaunch& a, const Fp8Entry& v, int t) {
   return (uint32_t)(v.hbase + (t & ~15)) * (uint32_t)a.e.hld;
@@ -90,9 +90,10 @@ __device__ __forceinline__ uint32_t h_tile(const Fp8ExpertLaunch& a, const Fp8En
 // A task is 8 RT pairs of an entry: RT tiles of 8 gate rows (p0 ..) and the 8
 // up rows of the same pairs.  The waves split d by blocks and meet in LDS,
 // where the gate sum of a pair finds its up sum.  At d = 7168 of 384 experts:
-// 1 token 13.3 us (a chain of router rows 2.6, selection 2.8 and one task 5),
-// 8 tokens 25.7 (112 MB: 4.7 of routing, then the stream), 64 tokens, I = 256,
-// 47.9 (200 MB, 4.2 TB/s: a compute unit's intake of weights and activations).
+// 1 token 13.2 us (a chain of router rows 2.6, selection 2.8 and one task 5),
+// 8 tokens 25.8 (112 MB: 4.7 of routing, then the stream), 64 tokens, I = 256,
+// 47.7 (200 MB: 4.2 of plan, then 5.9 TB/s until workgroups end, from 34 on;
+// the last at 46: tasks of 8 to 34 us).
 
 constexpr int kFp8Pairs = 8;
 constexpr int kKeysMaxTokens = 2;
@@ -326,8 +327,8 @@ __global__ __launch_bounds__(UpFp8<MAXB>::kWaves * 64, MAXB <= 8 ? 1 : kUpManyWg
 // outputs in an LDS tile, which is then combined in the order of combine_one.
 // A wave requests the next entry's rows and scales before it multiplies
 // the current one.  h is a pair of bf16 planes, so a step of the
-// product is two matrix instructions.  The same workloads: 5.9, 14.9 (56 MB,
-// 3.7 TB/s) and 29.2 us (102 MB, 3.5 TB/s); every compute unit reads all of h,
+// product is two matrix instructions.  The same workloads: 5.8, 14.7 (56 MB,
+// 3.8 TB/s) and 28.0 us (102 MB, 3.7 TB/s); every compute unit reads all of h,
 // which bounds it beside the rows.
 
 template <int RT, int KBM>

@@ -178,7 +178,7 @@ hipError_t launch_quantize(const QuantizeLaunch& a0, hipStream_t st) {
 // and meet once, in LDS, in wave order (deterministic).  Bound by the bytes of
 // W where there are many row groups (7168 x 7168, 5 tokens: 51.5 MB in 10.8
 // us, 4.8 TB/s), else by the latency of its K steps (2304 x 7168, 8 tokens:
-// 144 groups, 7.1 us; 7168 x 2048, 1 token, all of K in flight: 5.6 us).
+// 144 groups, 7.0 us; 7168 x 2048, 1 token, all of K in flight: 5.2 us).
 
 // Results of token t, rows n .. n + 3 (only those below N are there): with N a
 // multiple of 4 one store, r the residual's 4 bf16 (zeros without one).
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(MAXW * 64) void gemm_fp8_kernel(GemmFp8Launch a) {
 // More than 16 tokens: 64 RT rows of W and one of a.ks_n slices of K for each
 // workgroup (shared_product).  The slices' sums meet in the workspace: the
 // last workgroup of a row group to arrive adds them in slice order.  7168 x
-// 7168, 64 tokens of e4m3 with a residual: 22.9 us, of which the start takes
+// 7168, 64 tokens of e4m3 with a residual: 22.5 us, of which the start takes
 // about 2.7, the blocks 12 (4.3 TB/s of W; bound by the activations' way
 // through LDS), the arrival 2, the slices' sums 3.  Rows dealt evenly over all
 // compute units (28 instead of 32 a wave) gained nothing: 24.1 us against 24.1.
@@ -401,9 +401,9 @@ static void go(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
 }
 
 // Which kernel takes a product of more than 16 tokens, measured at B = 64 or
-// 32 (us, shared against split waves): 7168 x 7168 bf16 22.0 / 24.4, e4m3
-// 23.7 / 23.0; 1536 x 7168 10.5 / 12.3 (bf16, 32), 14.0 / 17.4 (e4m3, 64);
-// 7168 x 2048 (e4m3, 32) 10.6 / 6.5; 1001 x 1040 8.5 / 5.3.  A short K leaves
+// 32 (us, shared against split waves): 7168 x 7168 bf16 22.3 / 30.4, e4m3
+// 23.8 / 23.4; 1536 x 7168 10.8 / 12.5 (bf16, 32), 13.5 / 18.7 (e4m3, 64);
+// 7168 x 2048 (e4m3, 32) 11.0 / 6.6; 1001 x 1040 (33) 8.7 / 5.1.  A short K leaves
 // the shared kernel too few blocks to hide its start and its meeting.
 constexpr int kSharedMinTokens = 17, kSharedMinK = 4096;
 
@@ -411,7 +411,7 @@ constexpr int kSharedMinTokens = 17, kSharedMinK = 4096;
 // many slices as put a workgroup on every compute unit, of at least four
 // blocks (two a half), while the last workgroup of a row group reads at most
 // kMaxPartialBytes (one or two round trips).  RT = 2 from N = 6400 on: at
-// N = 7168 22.0 us against 26.2 with RT = 1, at 1536 no difference.
+// N = 7168 22.3 us against 26.0 with RT = 1, at 1536 no difference.
 GemmFp8Plan gemm_fp8_plan(int M, int N, int K) {
   constexpr int kCUs = 256, kMaxPartialBytes = 128 * 1024, kMinNForTwo = 6400;
   GemmFp8Plan p = {0, 1, 0};
@@ -438,7 +438,8 @@ static void go_shared(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
 }
 
 // Two row tiles a wave (half the activation bytes for a weight byte) once the
-// rows still make a workgroup for every other compute unit.
+// rows still make a workgroup for every other compute unit: 33 x 7168 x 2048
+// 9.9 us against 11.9 with one, 64 x 4608 x 2048 11.5 against 13.8.
 constexpr int kMinNForTwoTiles = 4096;
 
 hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
@@ -449,7 +450,7 @@ hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* sha
     b.ks_n = p.ks;
     auto pick = [&](auto E) {
       constexpr bool E8 = decltype(E)::value;
-      constexpr int U = 2;   // 7168 x 7168, B = 64: 22.0 us, 24.4 at 3, 25.1 at 4 (registers)
+      constexpr int U = 2;   // 7168 x 7168, B = 64: 22.3 us, 24.3 at 3, 24.8 at 4 (registers); 1536 x 7168 13.5, 14.4, 13.8
       if (p.rt == 1) {
         if (nt == 2) go_shared<1, 2, E8, U>(b, st, shape);
         else if (nt == 3) go_shared<1, 3, E8, U>(b, st, shape);
@@ -464,13 +465,20 @@ hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* sha
     else pick(std::false_type());
     return hipGetLastError();
   }
-  // Waves and blocks in flight: up to 8 tokens 8 waves of 2 blocks (two or
-  // more workgroups a compute unit; 7168 x 7168, B = 1: 10.8 us against 12.9
-  // with 14 waves of 4), up to 16 tokens 4 waves of 2 (16.1 against 18.9 with
-  // 8 of 4), beyond that 4 waves.
+  // Blocks in flight of a wave and waves, up to 16 tokens.  More of the first
+  // pays over a row of 2048 columns or more (below, it leaves three waves or
+  // fewer); with 5 tokens and more, or e4m3 ones, only where every compute
+  // unit has a row group (many).  Measured, us, this against the other choice:
+  //   <= 4 tokens:       1 x 7168 x 7168 10.4 / 10.9, 1 x 7168 x 2048 5.0 / 5.2; 2 x 7168 x 512 3.4 / 3.45
+  //   <= 8, e4m3:        5 x 7168 x 7168 11.2 / 11.5; 7 x 1536 x 4096 5.2 / 5.5, 1 x 16384 x 1024 5.4 / 5.5
+  //   5 to 8:            8 x 57344 x 7168 73.7 / 76.0; 8 x 2304 x 7168 7.6 / 7.7; 8 x 7168 x 2048 5.7 / 5.8, 6 x 1024 x 1536 3.56 / 3.65
+  //   9 to 16 (waves):   e4m3 16 x 7168 x 7168 13.8 / 14.5, 12 x 2304 x 7168 8.0 / 8.9; bf16 16 x 4096 x 4096 7.7 / 7.9
+  const bool many = a.N >= 16 * 256, lengthy = a.K >= 2048;
   if (a.x_e4m3) {
-    if (a.M <= 8) go<X8P, 1, 1, 2, 8>(a, st, shape);
-    else if (nt <= 1) go<X8, 1, 1, 2, 4>(a, st, shape);
+    if (a.M <= 8 && many && lengthy) go<X8P, 1, 1, 4, 8>(a, st, shape);
+    else if (a.M <= 8) go<X8P, 1, 1, 2, 8>(a, st, shape);
+    else if (nt <= 1 && many) go<X8, 1, 1, 2, 4>(a, st, shape);
+    else if (nt <= 1) go<X8, 1, 1, 2, 8>(a, st, shape);
     else if (a.N < kMinNForTwoTiles) {
       if (nt == 2) go<X8, 1, 2, 2, 8>(a, st, shape);
       else if (nt == 3) go<X8, 1, 3, 2, 8>(a, st, shape);
@@ -481,10 +489,14 @@ hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* sha
       else go<X8, 2, 4, 2, 4>(a, st, shape);
     }
   } else {
-    if (a.M <= 4) go<XP4, 1, 1, 2, 8>(a, st, shape);
-    else if (a.M <= 8 && a.K <= 8 * 2 * kQBlock) go<XP8, 1, 1, 2, 8>(a, st, shape);   // one step of 8 waves x 2 blocks
+    if (a.M <= 4 && lengthy) go<XP4, 1, 1, 4, 8>(a, st, shape);
+    else if (a.M <= 4) go<XP4, 1, 1, 2, 8>(a, st, shape);
+    else if (a.M <= 8 && !lengthy) go<XP8, 1, 1, 2, 8>(a, st, shape);
+    else if (a.M <= 8 && a.K <= 2048) go<XP8, 1, 1, 4, 8>(a, st, shape);   // all of the row in one step
+    else if (a.M <= 8 && many) go<XP8L, 1, 1, 3, 8>(a, st, shape);
     else if (a.M <= 8) go<XP8L, 1, 1, 2, 8>(a, st, shape);
-    else if (nt <= 1) go<XB, 1, 1, 2, 4>(a, st, shape);
+    else if (nt <= 1 && many) go<XB, 1, 1, 2, 4>(a, st, shape);
+    else if (nt <= 1) go<XB, 1, 1, 2, 8>(a, st, shape);
     else if (a.N < kMinNForTwoTiles) {
       if (nt == 2) go<XB, 1, 2, 2, 8>(a, st, shape);
       else if (nt == 3) go<XB, 1, 3, 2, 8>(a, st, shape);

@@ -169,6 +169,19 @@ def test_gemm_rows_of_several_steps(B, N, K):
         Y.check()
 
 
+@pytest.mark.parametrize("xt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,N,K", [(4, 4097, 2032), (4, 40, 2048), (2, 33, 8208), (8, 4096, 2048), (5, 4095, 2048), (7, 4100, 2064), (13, 4096, 144),
+                                   (16, 4095, 272)])
+def test_gemm_beside_the_limits_of_each_shape(B, N, K, xt):
+    # row groups and columns on both sides of where the blocks in flight and the waves change
+    c = Dense(B, N, K, xt)
+    Y = Guarded((B, N), torch.bfloat16)
+    c.call(Y.t, dev(c.R))
+    torch.cuda.synchronize()
+    c.check(host(Y.t), True, "bf16")
+    Y.check()
+
+
 @pytest.mark.parametrize("B,N,K,xt", [(3, 130, 400, "bf16"), (20, 130, 400, "bf16"), (20, 130, 400, "e4m3")])
 def test_gemm_small_integers_are_exact(B, N, K, xt):
     """Codes of small integers, scales of powers of two: every sum is exact in fp32, whatever its order."""
