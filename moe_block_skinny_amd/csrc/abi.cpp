@@ -309,9 +309,9 @@ constexpr int kMaxN8 = 1 << 24;
 // Dense product over 8-bit weights: after the header, the K slices' sums.
 // The row groups' arrival counters are the header's words from 32 on: with
 // more than one slice there are at most 128 of them.
-size_t gemm_fp8_ws(int B, int N, int K) {
+size_t gemm_fp8_ws(int x_e4m3, int B, int N, int K) {
   if (B > kMaxB || N > kMaxN8 || K > kMaxK8) return 0;   // refused by the call; the plan's sums would pass 31 bits
-  const size_t part = gemm_fp8_plan(B, N, K).part_bytes;
+  const size_t part = gemm_fp8_plan(x_e4m3, B, N, K).part_bytes;
   return part ? up(kHeaderBytes + part) : 0;
 }
 
@@ -577,7 +577,7 @@ size_t moe_workspace_bytes(int op, int dtype, int B, int d, int E, int k, int I,
       return skinny_ws(B, E + N, d, bf16, true).total;
     case MOE_OP_SKINNY_GEMM_FP8:
       if (N <= 0 || K <= 0) return 0;
-      return gemm_fp8_ws(B, N, K);
+      return gemm_fp8_ws(dtype == MOE_DT_E4M3, B, N, K);
     case MOE_OP_BLOCK_FP8:
       if (E <= 0 || d <= 0 || k <= 0 || I < 0 || Is < 0) return 0;
       if (B > kMaxB || E > kMaxE || k > kMaxK || d > kMaxK8 || I > kMaxI || Is > kMaxI) return 0;
@@ -1200,7 +1200,7 @@ moe_status_t skinny_gemm_fp8(int x_dtype, int B, int N, int K, const void* X, co
   a.M = B;
   a.N = N;
   a.K = K;
-  const size_t need = gemm_fp8_ws(B, N, K);
+  const size_t need = gemm_fp8_ws(a.x_e4m3, B, N, K);
   if (need && !aligned(ws)) return fail(MOE_EINVAL, "ws null or misaligned");
   if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
   if (need) {

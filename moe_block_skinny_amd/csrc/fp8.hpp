@@ -33,13 +33,14 @@ struct GemmFp8Launch {
   uint32_t* counter;
 };
 
-// Shape of the product for more than 16 tokens: row tiles a wave, K slices,
-// bytes of the slices' sums in the workspace (0: one slice).
+// Shape of the product for many tokens over a long K (rt = 0: split waves take
+// it): row tiles a wave, K slices, bytes of the slices' sums in the workspace
+// (0: one slice).
 struct GemmFp8Plan {
   int rt, ks;
   size_t part_bytes;
 };
-GemmFp8Plan gemm_fp8_plan(int M, int N, int K);
+GemmFp8Plan gemm_fp8_plan(int x_e4m3, int M, int N, int K);
 
 // The block's expert launches over 8-bit weights: ExpertLaunch with W13, W2,
 // Ws13, Ws2 in e4m3 and their scales, one row of scales for each 128 gate

@@ -268,13 +268,13 @@ __global__ __launch_bounds__(MAXW * 64) void gemm_fp8_kernel(GemmFp8Launch a) {
   }
 }
 
-// More than 16 tokens: 64 RT rows of W and one of a.ks_n slices of K for each
-// workgroup (shared_product).  The slices' sums meet in the workspace: the
-// last workgroup of a row group to arrive adds them in slice order.  7168 x
-// 7168, 64 tokens of e4m3 with a residual: 22.5 us, of which the start takes
-// about 2.7, the blocks 12 (4.3 TB/s of W; bound by the activations' way
-// through LDS), the arrival 2, the slices' sums 3.  Rows dealt evenly over all
-// compute units (28 instead of 32 a wave) gained nothing: 24.1 us against 24.1.
+// Many tokens (split_waves_win: how many): 64 RT rows of W and one of a.ks_n
+// slices of K for each workgroup (shared_product).  The slices' sums meet in
+// the workspace: the last workgroup of a row group to arrive adds them in slice
+// order.  7168 x 7168, 64 bf16 tokens: 22.3 us, of which the start takes about
+// 2.7, the blocks 12 (4.3 TB/s of W; bound by the activations' way through
+// LDS), the arrival 2, the slices' sums 3.  Rows dealt evenly over all compute
+// units (28 instead of 32 a wave) gained nothing: 23.0 us against 22.4.
 template <int RT, int NT, bool E8, int U>
 __global__ __launch_bounds__(kSharedWaves * 64) void gemm_fp8_shared_kernel(GemmFp8Launch a) {
   extern __shared__ __align__(16) char s_lds[];
@@ -400,22 +400,41 @@ static void go(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
   *shape = {g, w, 16 * RT, NT * XTraits<XK>::kTokens, 1};
 }
 
-// Which kernel takes a product of more than 16 tokens, measured at B = 64 or
-// 32 (us, shared against split waves): 7168 x 7168 bf16 22.3 / 30.4, e4m3
-// 23.8 / 23.4; 1536 x 7168 10.8 / 12.5 (bf16, 32), 13.5 / 18.7 (e4m3, 64);
-// 7168 x 2048 (e4m3, 32) 11.0 / 6.6; 1001 x 1040 (33) 8.7 / 5.1.  A short K leaves
-// the shared kernel too few blocks to hide its start and its meeting.
+// Two row tiles a wave (half the activation bytes for a weight byte) once the
+// rows still make a workgroup for every other compute unit: 33 x 7168 x 2048
+// 9.9 us against 11.9 with one, 64 x 4608 x 2048 11.5 against 13.8.
+constexpr int kMinNForTwoTiles = 4096;
+
+// Which kernel takes a product of more than 16 tokens.  Split waves read the
+// activations for every 32 rows (16 below N = 4096), the shared kernel for
+// every 64 or 128, but has a start and a meeting of about 7 us to hide, which a
+// short K does not.  By the activation bytes of a column (tokens x bytes), us,
+// shared against split waves:
+//   one round of 32-row groups, 7168 x 7168: e4m3 17 tokens 18.2 / 13.6, 48
+//     21.5 / 19.2, 64 23.2 / 23.1; bf16 17 17.4 / 14.4, 32 17.9 / 17.0, 48
+//     20.9 / 25.4, 64 22.4 / 30.6; 4608 x 7168: e4m3 48 20.0 / 18.4, 64 21.4 /
+//     22.2; bf16 32 15.8 / 16.2, 48 18.3 / 24.7
+//   fewer rows: 2304 x 7168 e4m3 17 11.2 / 9.3, 32 11.4 / 11.8, 48 13.8 / 15.6;
+//     bf16 32 11.1 / 12.9
+//   more: 16384 x 7168 e4m3 17 28.4 / 23.2, 32 28.3 / 27.9, 48 31.6 / 34.5;
+//     bf16 17 27.1 / 26.4, 32 26.9 / 30.5; 32768 x 4096 e4m3 32 29.2 / 32.1
+//   short K: 7168 x 2048 (e4m3, 32) 11.0 / 6.6; 1001 x 1040 (bf16, 33) 8.7 / 5.1
 constexpr int kSharedMinTokens = 17, kSharedMinK = 4096;
+static bool split_waves_win(int x_e4m3, int M, int N) {
+  const int column = M * (x_e4m3 ? 1 : 2);
+  if (N >= kMinNForTwoTiles && N <= 32 * 256) return column <= 64;
+  return N <= 2 * 32 * 256 && column <= 32;
+}
 
 // K slices and row tiles of the shared kernel: 64 RT rows a workgroup, and as
 // many slices as put a workgroup on every compute unit, of at least four
 // blocks (two a half), while the last workgroup of a row group reads at most
 // kMaxPartialBytes (one or two round trips).  RT = 2 from N = 6400 on: at
 // N = 7168 22.3 us against 26.0 with RT = 1, at 1536 no difference.
-GemmFp8Plan gemm_fp8_plan(int M, int N, int K) {
+GemmFp8Plan gemm_fp8_plan(int x_e4m3, int M, int N, int K) {
   constexpr int kCUs = 256, kMaxPartialBytes = 128 * 1024, kMinNForTwo = 6400;
   GemmFp8Plan p = {0, 1, 0};
-  if (M < kSharedMinTokens || K < kSharedMinK) return p;
+  if (M < kSharedMinTokens || K < kSharedMinK || split_waves_win(x_e4m3, M, N)) return p;
   const int KB = (K + kQBlock - 1) / kQBlock, nt = (M + 15) / 16;
   p.rt = N >= kMinNForTwo ? 2 : 1;
   const int rg = (N + 64 * p.rt - 1) / (64 * p.rt);
@@ -437,13 +456,8 @@ static void go_shared(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
   *shape = {g, kSharedWaves, 64 * RT, 16 * NT, a.ks_n};
 }
 
-// Two row tiles a wave (half the activation bytes for a weight byte) once the
-// rows still make a workgroup for every other compute unit: 33 x 7168 x 2048
-// 9.9 us against 11.9 with one, 64 x 4608 x 2048 11.5 against 13.8.
-constexpr int kMinNForTwoTiles = 4096;
-
 hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* shape) {
-  const GemmFp8Plan p = gemm_fp8_plan(a.M, a.N, a.K);
+  const GemmFp8Plan p = gemm_fp8_plan(a.x_e4m3, a.M, a.N, a.K);
   const int nt = (a.M + 15) / 16;
   if (p.rt) {
     GemmFp8Launch b = a;
@@ -452,7 +466,7 @@ hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* sha
       constexpr bool E8 = decltype(E)::value;
       constexpr int U = 2;   // 7168 x 7168, B = 64: 22.3 us, 24.3 at 3, 24.8 at 4 (registers); 1536 x 7168 13.5, 14.4, 13.8
       if (p.rt == 1) {
-        if (nt == 2) go_shared<1, 2, E8, U>(b, st, shape);
+        if (nt == 2) go_shared<1, 2, false, U>(b, st, shape);   // bf16 (below)
         else if (nt == 3) go_shared<1, 3, E8, U>(b, st, shape);
         else go_shared<1, 4, E8, U>(b, st, shape);
       } else {
@@ -461,6 +475,8 @@ hipError_t launch_gemm_fp8(const GemmFp8Launch& a, hipStream_t st, Fp8Shape* sha
         else go_shared<2, 4, E8, U>(b, st, shape);
       }
     };
+    // up to 32 tokens of e4m3 and fewer than 6400 rows are split waves'
+    if (a.x_e4m3 && p.rt == 1 && nt == 2) return hipErrorInvalidValue;
     if (a.x_e4m3) pick(std::true_type());
     else pick(std::false_type());
     return hipGetLastError();

@@ -169,6 +169,18 @@ def test_gemm_rows_of_several_steps(B, N, K):
         Y.check()
 
 
+@pytest.mark.parametrize("B,N,K,xt", [(17, 100, 4112, "bf16"), (33, 200, 4096, "e4m3"), (64, 100, 4112, "e4m3"), (33, 6400, 4112, "bf16"),
+                                      (64, 6401, 4096, "bf16"), (17, 8193, 4096, "bf16"), (34, 8196, 4112, "e4m3"), (49, 8193, 4096, "e4m3"),
+                                      (20, 16400, 4096, "e4m3"), (32, 8192, 4096, "bf16"), (64, 8192, 4096, "e4m3"), (32, 4095, 4096, "e4m3")])
+def test_gemm_many_tokens_beside_the_limits_of_each_kernel(B, N, K, xt):
+    c = Dense(B, N, K, xt)
+    Y = Guarded((B, N), torch.bfloat16)
+    c.call(Y.t, dev(c.R))
+    torch.cuda.synchronize()
+    c.check(host(Y.t), True, "bf16")
+    Y.check()
+
+
 @pytest.mark.parametrize("xt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,N,K", [(4, 4097, 2032), (4, 40, 2048), (2, 33, 8208), (8, 4096, 2048), (5, 4095, 2048), (7, 4100, 2064), (13, 4096, 144),
                                    (16, 4095, 272)])
