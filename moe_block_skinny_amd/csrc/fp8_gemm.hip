@@ -176,9 +176,11 @@ hipError_t launch_quantize(const QuantizeLaunch& a0, hipStream_t st) {
 //
 // A workgroup owns 16 RT rows of W over all of K; its waves split K by blocks
 // and meet once, in LDS, in wave order (deterministic).  Bound by the bytes of
-// W where there are many row groups (7168 x 7168, 5 tokens: 51.5 MB in 10.8
-// us, 4.8 TB/s), else by the latency of its K steps (2304 x 7168, 8 tokens:
-// 144 groups, 7.0 us; 7168 x 2048, 1 token, all of K in flight: 5.2 us).
+// W where there are many row groups (7168 x 7168, 5 tokens: 51.5 MB in 10.5
+// us, 4.9 TB/s), else by the latency of its K steps (2304 x 7168, 8 tokens:
+// 144 groups, 7.0 us; 7168 x 2048, 1 token, all of K in flight: 5.2 us); with
+// 64 tokens by instruction issue (7168 x 7168, e4m3: 22.4 us, of a wave's
+// cycles 17 % wait for data).
 
 // Results of token t, rows n .. n + 3 (only those below N are there): with N a
 // multiple of 4 one store, r the residual's 4 bf16 (zeros without one).
